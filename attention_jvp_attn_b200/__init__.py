@@ -19,11 +19,14 @@ import torch
 from . import _abi
 from ._abi import AttnJvpError  # noqa: F401
 from .inputs import BLOCK_CAUSAL, TEACHER_FORCING  # noqa: F401
+from .serving import (PagedCache, cache_append, cache_attn, paged_cache,  # noqa: F401
+                      prompt_attn, rope_at, rope_tables)
 
 __all__ = ["attn_jvp", "attn_jvp_groups", "attn_jvp_bwd", "attn_jvp_bwd_groups", "rope",
            "attn_jvp_rope", "attn_jvp_host", "sync_status", "unmasked_pairs", "schedule_tiles",
            "key_tile_query_bounds", "host_staging_bytes", "AttnJvpError", "TEACHER_FORCING",
-           "BLOCK_CAUSAL"]
+           "BLOCK_CAUSAL", "rope_at", "rope_tables", "PagedCache", "paged_cache", "cache_append",
+           "cache_attn", "prompt_attn"]
 
 _DT = {torch.bfloat16: _abi.DTYPE_BF16, torch.float32: _abi.DTYPE_F32}
 

@@ -16,9 +16,14 @@ ERR_MISALIGNED = 3
 ERR_CUDA = 4
 ERR_DEVICE_TIMEOUT = 5
 ERR_NO_DEVICE = 6
+ERR_BAD_INDEX = 7
 
 DTYPE_BF16 = 0
 DTYPE_F32 = 1
+DTYPE_F16 = 2  # the serving operators only
+
+ROPE_INTERLEAVED = 0
+ROPE_HALF = 1
 
 
 class Shape(ctypes.Structure):
@@ -29,6 +34,29 @@ class Shape(ctypes.Structure):
 class Mask(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int32), ("chunk_tokens", ctypes.c_int32),
                 ("n_chunks", ctypes.c_int32)]
+
+
+class Tokens(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("Hkv", ctypes.c_int64),
+                ("d", ctypes.c_int64), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class RopeTables(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+                ("n_positions", ctypes.c_int64), ("rot", ctypes.c_int64),
+                ("layout", ctypes.c_int32)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_tokens", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
 
 
 MAX_GROUPS = 512
@@ -115,6 +143,22 @@ def load(path: str = None) -> ctypes.CDLL:
         lib.attn_jvp_fwd_rope.restype = ctypes.c_int
         lib.attn_jvp_debug_wait.argtypes = [ctypes.c_int64, ctypes.c_int32]
         lib.attn_jvp_debug_wait.restype = ctypes.c_int
+        i64, i32 = ctypes.c_int64, ctypes.c_int32
+        lib.attn_jvp_rope_at.argtypes = [ctypes.POINTER(Tokens), vp, Strides, vp, Strides, vp, i32,
+                                         ctypes.POINTER(RopeTables), i32, vp, Strides, vp,
+                                         Strides, vp]
+        lib.attn_jvp_rope_at.restype = ctypes.c_int
+        lib.attn_jvp_cache_append.argtypes = [ctypes.POINTER(Tokens), vp, Strides, vp, Strides,
+                                              ctypes.POINTER(Cache), i64, vp, vp, vp, i64, i64,
+                                              ctypes.POINTER(RopeTables), vp]
+        lib.attn_jvp_cache_append.restype = ctypes.c_int
+        lib.attn_jvp_cache_attn.argtypes = [ctypes.POINTER(Shape), i64, vp, ctypes.POINTER(i64),
+                                            ctypes.POINTER(Cache), vp, vp, i64, i64, i64, i32, vp,
+                                            vp, vp]
+        lib.attn_jvp_cache_attn.restype = ctypes.c_int
+        lib.attn_jvp_prompt_attn.argtypes = [ctypes.POINTER(Tokens), vp, Strides, vp, Strides, vp,
+                                             Strides, i64, vp, vp, vp, vp]
+        lib.attn_jvp_prompt_attn.restype = ctypes.c_int
         lib.attn_jvp_version.argtypes = []
         lib.attn_jvp_version.restype = ctypes.c_int32
         _lib = lib

@@ -13,6 +13,7 @@
 
 #include "attn_jvp.h"
 #include "kernels.cuh"
+#include "ptx.cuh"
 
 namespace {
 
@@ -79,6 +80,14 @@ int device_state(DeviceState** out) {
       }
       g_encode = reinterpret_cast<EncodeTiledFn>(fn);
     }
+    // The first call on a device may fall inside a stream capture of this
+    // thread; its one-off set-up is not part of the graph, so it runs in the
+    // relaxed mode, which allows it.
+    struct RelaxedCapture {
+      cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+      RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+      ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    } relaxed;
     if (cudaMalloc(&st.status, kStateBytes) != cudaSuccess) {
       cudaGetLastError();
       st.status = nullptr;
@@ -525,6 +534,15 @@ int device_status_word(unsigned int** word) {
   return ATTN_JVP_OK;
 }
 
+int device_status_word(unsigned int** word, int* sm_count) {
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc != ATTN_JVP_OK) return rc;
+  *word = st->status;
+  *sm_count = st->sm_count;
+  return ATTN_JVP_OK;
+}
+
 bool encode_bf16_rows_map(CUtensorMap* map, const void* base, int64_t B, int64_t L, int64_t H,
                           int64_t d, int box_rows) {
   if (!g_encode) return false;
@@ -535,6 +553,26 @@ bool encode_bf16_rows_map(CUtensorMap* map, const void* base, int64_t B, int64_t
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_token_rows_map(CUtensorMap* map, const void* base, int32_t dtype, int64_t T,
+                           int64_t heads, int64_t d, int64_t token_stride, int64_t head_stride,
+                           int box_rows) {
+  if (!g_encode) return false;
+  // a stride that no second index uses may be anything: give the map a valid one
+  if (heads == 1) head_stride = d;
+  if (T == 1) token_stride = heads * d;
+  const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(T)};
+  const cuuint64_t strides[2] = {cuuint64_t(head_stride) * 2, cuuint64_t(token_stride) * 2};
+  const cuuint32_t box[3] = {64, 1, cuuint32_t(box_rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(map,
+                  dtype == ATTN_JVP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -705,7 +743,8 @@ int attn_jvp_sync_status(void* stream) {
   }
   if (word != 0) {
     cudaMemset(st->status, 0, sizeof(unsigned int));
-    return ATTN_JVP_ERR_DEVICE_TIMEOUT;
+    // a wait that ran out outweighs a bad index: it invalidates more
+    return (word & ajvp::kStatusTimeout) ? ATTN_JVP_ERR_DEVICE_TIMEOUT : ATTN_JVP_ERR_BAD_INDEX;
   }
   return ATTN_JVP_OK;
 }
@@ -719,6 +758,7 @@ const char* attn_jvp_status_string(int status) {
     case ATTN_JVP_ERR_CUDA: return "CUDA error";
     case ATTN_JVP_ERR_DEVICE_TIMEOUT: return "device wait timed out; outputs invalid";
     case ATTN_JVP_ERR_NO_DEVICE: return "no usable sm_100 device";
+    case ATTN_JVP_ERR_BAD_INDEX: return "a position, length or page on the device is out of range";
     default: return "unknown status";
   }
 }

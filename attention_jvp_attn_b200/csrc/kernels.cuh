@@ -104,9 +104,17 @@ int bwd_tc_launch(const BwdTcArgs& a, cudaStream_t stream);  // ATTN_JVP_* statu
 // The current device's status word (bit 0: a bounded wait ran out), set up
 // once per device; returns an ATTN_JVP_* status.
 int device_status_word(unsigned int** word);
+// The same, and the device's number of SMs.
+int device_status_word(unsigned int** word, int* sm_count);
 // 4-D tensor map over a dense [B, L, H, d] bf16 array: boxes of 64 columns x
 // `box_rows` rows of one (batch, head), 128-byte swizzle, zero fill out of range.
 bool encode_bf16_rows_map(CUtensorMap* map, const void* base, int64_t B, int64_t L, int64_t H,
                           int64_t d, int box_rows);
+// 3-D tensor map over a [T, heads, d] array of 2-byte elements (bf16 or fp16,
+// `dtype` an attn_jvp_dtype) with strides in elements: boxes of 64 columns x
+// `box_rows` tokens of one head, 128-byte swizzle, zero fill out of range.
+bool encode_token_rows_map(CUtensorMap* map, const void* base, int32_t dtype, int64_t T,
+                           int64_t heads, int64_t d, int64_t token_stride, int64_t head_stride,
+                           int box_rows);
 
 }  // namespace ajvp

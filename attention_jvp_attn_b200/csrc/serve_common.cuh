@@ -1,0 +1,187 @@
+// serve_common.cuh - what the serving operators share: element types as 32-bit
+// values, the checks of their arguments, the e4m3 conversions, and the search
+// for the sequence that a piece of packed work belongs to.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "attn_jvp.h"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace ajvp_serve {
+
+constexpr uint32_t kStatusBadIndex = 2u;  // bit of the device status word
+
+// ---- host: argument checks ----
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline int dtype_bytes(int32_t dtype) {
+  return dtype == ATTN_JVP_F32 ? 4 : (dtype == ATTN_JVP_BF16 || dtype == ATTN_JVP_F16) ? 2 : 0;
+}
+
+// A [rows, heads, d] array: pointer set and aligned, strides in whole 16 bytes.
+// A stride that no second index uses is not looked at.
+inline int check_rows(const void* p, attn_jvp_strides s, int64_t rows, int64_t heads, int bytes) {
+  if (!p) return ATTN_JVP_ERR_INVALID_ARGUMENT;
+  if (!aligned16(p)) return ATTN_JVP_ERR_MISALIGNED;
+  if ((rows > 1 && (s.token < 0 || s.token * bytes % 16)) ||
+      (heads > 1 && (s.head < 0 || s.head * bytes % 16)))
+    return ATTN_JVP_ERR_MISALIGNED;
+  return ATTN_JVP_OK;
+}
+
+// The same for an output: rows and heads must not fall on one another.
+inline int check_rows_out(const void* p, attn_jvp_strides s, int64_t rows, int64_t heads,
+                          int64_t d, int bytes) {
+  const int rc = check_rows(p, s, rows, heads, bytes);
+  if (rc != ATTN_JVP_OK) return rc;
+  const bool token_outside = (heads == 1 || s.head >= d) && (rows == 1 || s.token >= (heads - 1) * (heads > 1 ? s.head : 0) + d);
+  const bool head_outside = (rows == 1 || s.token >= d) && (heads == 1 || s.head >= (rows - 1) * (rows > 1 ? s.token : 0) + d);
+  return token_outside || head_outside ? ATTN_JVP_OK : ATTN_JVP_ERR_INVALID_ARGUMENT;
+}
+
+inline int check_tables(const attn_jvp_rope_tables* t, int64_t d) {
+  if (!t) return ATTN_JVP_ERR_INVALID_ARGUMENT;
+  if (!t->cos || !t->sin || t->n_positions < 1 || t->n_positions > (int64_t(1) << 31) - 1)
+    return ATTN_JVP_ERR_INVALID_ARGUMENT;
+  if (!aligned16(t->cos) || !aligned16(t->sin)) return ATTN_JVP_ERR_MISALIGNED;
+  if (t->rot < 16 || t->rot % 16 || t->rot > d) return ATTN_JVP_ERR_INVALID_ARGUMENT;
+  if (t->layout != ATTN_JVP_ROPE_INTERLEAVED && t->layout != ATTN_JVP_ROPE_HALF)
+    return ATTN_JVP_ERR_INVALID_ARGUMENT;
+  return ATTN_JVP_OK;
+}
+
+inline int check_cache(const attn_jvp_cache* c, int64_t Hkv, int64_t d) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return ATTN_JVP_ERR_INVALID_ARGUMENT;
+  if (c->pages < 1 || c->pages > (int64_t(1) << 31) - 1) return ATTN_JVP_ERR_INVALID_ARGUMENT;
+  if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128)
+    return ATTN_JVP_ERR_UNSUPPORTED;
+  if (!aligned16(c->k) || !aligned16(c->v)) return ATTN_JVP_ERR_MISALIGNED;
+  if (c->page_stride % 16 || c->head_stride % 16 || c->token_stride % 16)
+    return ATTN_JVP_ERR_MISALIGNED;
+  if (c->token_stride < d || (Hkv > 1 && c->head_stride < d) || (c->pages > 1 && c->page_stride < d) ||
+      (c->pages > 1 && c->scale_page_stride < 1) || (Hkv > 1 && c->scale_head_stride < 1))
+    return ATTN_JVP_ERR_INVALID_ARGUMENT;
+  return ATTN_JVP_OK;
+}
+
+// Raises a kernel's shared-memory limit once per device (`done`: devices that
+// have it; the kernel's own).
+template <typename F>
+cudaError_t allow_smem(F* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+// ---- device: element types ----
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+  static __device__ __forceinline__ void unpack(uint32_t w, float& a, float& b) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    return ajvp::pack_bf16x2(a, b);
+  }
+};
+template <>
+struct Elem<__half> {
+  static __device__ __forceinline__ void unpack(uint32_t w, float& a, float& b) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    a = f.x;
+    b = f.y;
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+// Eight adjacent elements as 32-bit values, and back.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    Elem<T>::unpack(u.x, x[0], x[1]);
+    Elem<T>::unpack(u.y, x[2], x[3]);
+    Elem<T>::unpack(u.z, x[4], x[5]);
+    Elem<T>::unpack(u.w, x[6], x[7]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(Elem<T>::pack(x[0], x[1]), Elem<T>::pack(x[2], x[3]),
+                   Elem<T>::pack(x[4], x[5]), Elem<T>::pack(x[6], x[7]));
+  }
+}
+
+__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+}
+
+// ---- device: e4m3 ----
+// Two values to two codes, to nearest even, beyond +-448 to the largest code.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two codes (the low 16 bits) to their values as an fp16 pair, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+  return r;
+}
+
+// The start of sequence b's rows in a packed array of T rows, from data that
+// may be out of order: always in [0, T], so that no row outside is touched.
+__device__ __forceinline__ int clamp_row(int start, int T) { return min(max(start, 0), T); }
+
+// Work over packed sequences is cut into pieces of `unit` rows. Sequence b
+// owns the pieces from starts[b] / unit + slack * b on: the next sequence's
+// first piece lies at least rows / unit + slack further, which is enough for
+// its rows however they straddle the pieces (slack = 1 for pieces that begin
+// with the sequence, 2 for pieces that may begin inside a page). So a block
+// finds its sequence by counting the first pieces at or before its own, in
+// one round of loads for up to blockDim.x sequences, and without any scan of
+// the lengths. Pieces that no sequence uses do nothing. Every thread of the
+// block calls this; the result is the same in all of them. It relies on
+// non-decreasing starts; others give some in-range sequence number.
+__device__ __forceinline__ int find_sequence(const int32_t* starts, int B, int T, int unit,
+                                             int slack, int piece) {
+  int before = 0;
+  for (int b0 = 0; b0 < B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    const bool in =
+        b < B && clamp_row(starts[b], T) / unit + static_cast<int64_t>(slack) * b <= piece;
+    before += __syncthreads_count(in);
+  }
+  return before > 0 ? before - 1 : 0;
+}
+
+}  // namespace ajvp_serve

@@ -66,7 +66,9 @@ enum {
   ATTN_JVP_ERR_MISALIGNED = 3,       /* a pointer is not 16-byte aligned */
   ATTN_JVP_ERR_CUDA = 4,             /* a CUDA runtime or driver call failed */
   ATTN_JVP_ERR_DEVICE_TIMEOUT = 5,   /* a kernel's bounded wait ran out; the outputs are invalid */
-  ATTN_JVP_ERR_NO_DEVICE = 6         /* no usable sm_100 device */
+  ATTN_JVP_ERR_NO_DEVICE = 6,        /* no usable sm_100 device */
+  ATTN_JVP_ERR_BAD_INDEX = 7         /* a position, length or page read on the device was out of range;
+                                        what it pointed at was neither read nor written */
 };
 
 /* ---- mask ------------------------------------------------------------ */
@@ -101,7 +103,8 @@ typedef struct {
 /* ---- problem --------------------------------------------------------- */
 typedef enum {
   ATTN_JVP_BF16 = 0, /* bf16 inputs/outputs, fp32 accumulation, tensor cores */
-  ATTN_JVP_F32 = 1   /* fp32 inputs/outputs, fp32 arithmetic on CUDA cores */
+  ATTN_JVP_F32 = 1,  /* fp32 inputs/outputs, fp32 arithmetic on CUDA cores */
+  ATTN_JVP_F16 = 2   /* fp16; only where a function below says so (the serving operators) */
 } attn_jvp_dtype;
 
 typedef struct {
@@ -465,6 +468,170 @@ int attn_jvp_debug_wait(int64_t limit_ns, int32_t stall_tile);
 
 /* Library version, major * 10000 + minor * 100 + patch. */
 int32_t attn_jvp_version(void);
+
+/* ======================================================================
+ * Serving operators: rotation at positions, a paged 8-bit key-value cache,
+ * the attention over it, and the causal attention of packed prompts.
+ *
+ * Token rows are [T, heads, d] arrays with a stride per token and per head
+ * (in elements; the d elements of a head are adjacent), so views of a fused
+ * projection can be passed. Every pointer is 16-byte aligned and every
+ * stride a multiple of 16 bytes. Query heads are grouped: query head h reads
+ * key head h / (H / Hkv); H is a multiple of Hkv.
+ *
+ * Positions, lengths and page numbers are device data, which the host cannot
+ * check without waiting for it. The kernels check each before they use it;
+ * one that is out of range is not used (each function says what becomes of
+ * its outputs: by default they are left as they were), and
+ * attn_jvp_sync_status reports ATTN_JVP_ERR_BAD_INDEX later.
+ *
+ * No function here synchronizes, allocates device memory or keeps state
+ * between calls, so each can be captured in a CUDA graph, and calls on
+ * several streams may overlap as long as their outputs do not.
+ * ====================================================================== */
+
+/* Packed token rows. */
+typedef struct {
+  int64_t T;     /* tokens >= 0 (T = 0: nothing is done) */
+  int64_t H;     /* query heads >= 1 (cache_append: ignored) */
+  int64_t Hkv;   /* key/value heads >= 1; H is a multiple of it */
+  int64_t d;     /* head dim: 64 or 128 */
+  int32_t dtype; /* attn_jvp_dtype */
+  float scale;   /* softmax scale s; <= 0 selects 1/sqrt(d) (attention only) */
+} attn_jvp_tokens;
+
+/* Strides of a [T, heads, d] array, in elements. */
+typedef struct {
+  int64_t token, head;
+} attn_jvp_strides;
+
+/* Which columns of a head form a pair in a rotation of its first `rot` columns. */
+typedef enum {
+  ATTN_JVP_ROPE_INTERLEAVED = 0, /* (2i, 2i + 1) */
+  ATTN_JVP_ROPE_HALF = 1         /* (i, i + rot/2) */
+} attn_jvp_rope_layout;
+
+/* Rotation tables: cos and sin [n_positions, rot/2] float, dense. */
+typedef struct {
+  const float* cos;
+  const float* sin;
+  int64_t n_positions;
+  int64_t rot;    /* columns rotated: a multiple of 16, <= d; the others are copied */
+  int32_t layout; /* attn_jvp_rope_layout */
+} attn_jvp_rope_tables;
+
+/*
+ * attn_jvp_rope_at - rotary embedding of queries and keys at given positions:
+ * for token t, p = positions[t] and each pair (a, b) of its columns,
+ *     a' = a cos[p] - b sin[p],   b' = a sin[p] + b cos[p]
+ * in fp32, rounded once. With transpose != 0 the transposed matrix (sin
+ * negated) is applied: the gradient with respect to q and k, given the
+ * gradients of the rotated ones. Scaled positions and a magnitude live in the
+ * tables.
+ *
+ *   shape      T, H (heads of q), Hkv (heads of k), d, dtype (all three types)
+ *   q, k       inputs with their strides; k may be NULL (then k_out too)
+ *   positions  T integers of position_bytes (4 or 8) each, 0 <= p < n_positions;
+ *              a token whose position is outside keeps its output rows as they were
+ *   q_out, k_out  outputs with their strides; each may be its own input
+ */
+int attn_jvp_rope_at(const attn_jvp_tokens* shape, const void* q, attn_jvp_strides q_strides,
+                     const void* k, attn_jvp_strides k_strides, const void* positions,
+                     int32_t position_bytes, const attn_jvp_rope_tables* tables, int32_t transpose,
+                     void* q_out, attn_jvp_strides q_out_strides, void* k_out,
+                     attn_jvp_strides k_out_strides, void* stream);
+
+/*
+ * A paged key-value cache in 8 bits. A page holds page_tokens tokens of every
+ * key head: e4m3 codes, and one fp32 scale per page and head; the value of a
+ * code c is c * scale. Strides are in elements (bytes for the codes), the
+ * same for k and v; the d codes of a token's head are adjacent.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages;       /* pages in the pool, >= 1 */
+  int64_t page_tokens; /* 16, 32, 64 or 128 */
+  int64_t page_stride, head_stride, token_stride;     /* of k and v; multiples of 16 */
+  int64_t scale_page_stride, scale_head_stride;       /* of k_scale and v_scale */
+} attn_jvp_cache;
+
+/*
+ * attn_jvp_cache_append - append tokens to the cache, the keys rotated on the
+ * way if tables are given. Token starts[b] + i of the packed rows becomes
+ * token p = cached[b] + i of sequence b: its key (rotated by position p) and
+ * value go to row p % page_tokens of page table[b][p / page_tokens].
+ *
+ * The scale of a page and head is a power of two: the smallest 2^e with
+ * |x| <= 448 * 2^e over the finite values x of the new tokens in the page,
+ * -32 <= e <= 32, and not below the page's scale before the call where the
+ * page keeps earlier tokens of the sequence. Where it grows, those tokens'
+ * codes are rounded anew to it (exact but for the smallest, subnormal codes).
+ * A value is rounded once, from fp32 to e4m3 (to nearest even); values beyond
+ * 448 * 2^e, infinities among them, become the largest code, NaN stays NaN.
+ * Rows of a page behind the last appended token are left as they were. Calling
+ * it twice with the same arguments gives the same cache.
+ *
+ *   shape    T = tokens in k and v; Hkv, d, dtype (all three types)
+ *   starts   [B + 1] int32, non-decreasing, starts[0] >= 0, starts[B] <= T;
+ *            rows outside them are ignored
+ *   cached   [B] int32, tokens of each sequence in the cache before the call
+ *   table    [B, table_width] int32 page numbers, table_stride apart; the pages
+ *            written belong to one sequence each
+ *   rope     NULL for no rotation; else n_positions must exceed every p
+ */
+int attn_jvp_cache_append(const attn_jvp_tokens* shape, const void* k, attn_jvp_strides k_strides,
+                          const void* v, attn_jvp_strides v_strides, const attn_jvp_cache* cache,
+                          int64_t B, const int32_t* starts, const int32_t* cached,
+                          const int32_t* table, int64_t table_width, int64_t table_stride,
+                          const attn_jvp_rope_tables* rope, void* stream);
+
+/*
+ * attn_jvp_cache_attn - attention of the newest n tokens of each sequence over
+ * its cached keys and values:
+ *     O = softmax(s Q K^T) V,   LSE = log sum exp(s Q K^T)   (natural log)
+ * over the keys j < lens[b] (causal == 0), or j < lens[b] - n + i + 1 for query
+ * i of n (causal != 0: the n queries are the sequence's last n tokens). A row
+ * that sees no key gets O = 0, LSE = -infinity.
+ *
+ *   shape   B = sequences, L = n, H, d, dtype (bf16 or fp16), scale
+ *   Hkv     key/value heads
+ *   q       [B, n, H, d]: q_strides[0..2] in elements for B, n, H
+ *   lens    [B] int32, tokens of each sequence in the cache, the new ones
+ *           included; <= table_width * page_tokens
+ *   table   as for attn_jvp_cache_append
+ *   max_len an upper bound of lens known on the host, or 0 for
+ *           table_width * page_tokens; it sets how the work is split, and longer
+ *           sequences are still computed whole
+ *   o       [B, n, H, d] dense, of dtype;  lse [B, H, n] float dense
+ *
+ * Scales in the cache are read as at least 2^-40 and at most 2^40. A sequence
+ * whose length is out of range gets the empty row's result, and the tokens of
+ * a page whose number is out of range count as hidden.
+ */
+int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, const void* q,
+                        const int64_t* q_strides, const attn_jvp_cache* cache,
+                        const int32_t* lens, const int32_t* table, int64_t table_width,
+                        int64_t table_stride, int64_t max_len, int32_t causal, void* o, float* lse,
+                        void* stream);
+
+/*
+ * attn_jvp_prompt_attn - causal attention inside each of B packed sequences:
+ * rows starts[b] <= t < starts[b + 1] of q, k and v, query t seeing keys
+ * starts[b] <= j <= t. Nothing outside a row's keys reaches it, infinities
+ * and NaN in masked rows included. Rows outside the sequences are left as
+ * they were.
+ *
+ *   shape   T, H, Hkv, d, dtype (bf16 or fp16), scale
+ *   starts  [B + 1] int32, as for attn_jvp_cache_append
+ *   o       [T, H, d] dense, of dtype;  lse [H, T] float dense
+ */
+int attn_jvp_prompt_attn(const attn_jvp_tokens* shape, const void* q, attn_jvp_strides q_strides,
+                         const void* k, attn_jvp_strides k_strides, const void* v,
+                         attn_jvp_strides v_strides, int64_t B, const int32_t* starts, void* o,
+                         float* lse, void* stream);
 
 #ifdef __cplusplus
 }
