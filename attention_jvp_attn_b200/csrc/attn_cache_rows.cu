@@ -58,12 +58,6 @@ __device__ __forceinline__ int v_place(int r, int q) {
                   : (r >> 1) * 128 + (((((r & 1) << 2) + q) ^ (((r >> 1) & 3) << 1)) << 4);
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -75,12 +69,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   return Elem<__half>::pack(a, b);
-}
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
 }
 
 template <typename T, int D>
@@ -544,15 +532,19 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
   p.scale_log2 = scale * 1.4426950408889634f;
   const int64_t bound = table_width * cache->page_tokens;
   const int64_t len = max_len > 0 && max_len < bound ? max_len : bound;
-  const int64_t row_tiles = (s.L * p.group + kRowsTile - 1) / kRowsTile;
+  const int64_t rows = s.L * p.group;
+  const bool few = rows <= kRowsTile;
+  const int per_tile = few ? kRowsTile : kTilesRows;
+  const int64_t row_tiles = (rows + per_tile - 1) / per_tile;
   const int64_t tiles = s.B * Hkv * row_tiles;
-  if (tiles > (int64_t(1) << 27)) return ATTN_JVP_ERR_UNSUPPORTED;
+  if (rows > (int64_t(1) << 30) || tiles > (int64_t(1) << 27)) return ATTN_JVP_ERR_UNSUPPORTED;
   p.row_tiles = static_cast<int>(row_tiles);
-  int splits = 1;
-  while (splits < 8 && tiles * splits < 2 * sms && len >= 256 * splits) splits *= 2;
-  p.splits = splits;
-  const cudaError_t e =
-      cache_rows_launch(p, static_cast<int>(s.d), s.dtype, static_cast<cudaStream_t>(stream));
+  p.splits = 1;
+  if (few)
+    while (p.splits < 8 && tiles * p.splits < 2 * sms && len >= 256 * p.splits) p.splits *= 2;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = few ? cache_rows_launch(p, static_cast<int>(s.d), s.dtype, st)
+                            : cache_tiles_launch(p, len, static_cast<int>(s.d), s.dtype, st);
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? ATTN_JVP_OK : ATTN_JVP_ERR_CUDA;
 }

@@ -58,7 +58,7 @@ struct PromptCfg {
   static constexpr int TILE = kTile * D * 2;
   static constexpr int NS = D == 128 ? 5 : 10;  // ring slots, K and V tiles in turn
   static constexpr int DATA = (2 + NS) * TILE;
-  static constexpr int NBAR = 2 * NS + 6 * 2 + 1;
+  static constexpr int NBAR = 2 * NS + 7 * 2 + 1;
   static constexpr int BYTES = 1024 + DATA + NBAR * 8 + 2 * 4 * 4 + 16;
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S_t at 128 t, O_t at 256 + D t
   static_assert(BYTES <= 232448, "shared memory budget");
@@ -69,6 +69,73 @@ template <bool F16>
 __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
   return F16 ? (((w & 0x7c007c00u) + 0x04000400u) >> 15) & 0x00010001u
              : (((w & 0x7f807f80u) + 0x00800080u) >> 15) & 0x00010001u;
+}
+
+// The rank-th pair of row tiles of all sequences, those that see the most keys
+// first (so that the blocks started last are short, whatever the sequences'
+// order): its sequence b and its index k in it. Pairs of index k or above
+// number sum_b max(0, pairs(b) - k), so k is found by bisection and b among
+// the sequences that have a pair k. Every thread of the block calls this; false
+// if there are not so many pairs. The cost is one round of loads and log2 T /
+// 256 sums over the block.
+__device__ __forceinline__ bool find_pair(const PromptParams& p, int rank, int& b, int& k) {
+  __shared__ int sums[kThreads / 32];
+  __shared__ int found;
+  const int warp = threadIdx.x >> 5;
+  auto pairs = [&](int i) -> int {
+    if (i >= p.B) return 0;
+    const int raw0 = p.starts[i], raw1 = p.starts[i + 1];
+    const int t0 = clamp_row(raw0, p.T), t1 = clamp_row(raw1, p.T);
+    if (t0 != raw0 || t1 != raw1 || t1 < t0) atomicOr(p.status, kStatusBadIndex);
+    return t1 > t0 ? (t1 - t0 + 2 * kTile - 1) / (2 * kTile) : 0;
+  };
+  const int own = pairs(threadIdx.x);  // the first kThreads sequences stay in registers
+  auto total = [&](int x) -> int {     // over the block
+    x = __reduce_add_sync(0xffffffffu, x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sums[warp] = x;
+    __syncthreads();
+    x = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) x += sums[w];
+    return x;
+  };
+  auto from = [&](int at) -> int {  // pairs of index `at` or above
+    int x = max(own - at, 0);
+    for (int i = threadIdx.x + kThreads; i < p.B; i += kThreads) x += max(pairs(i) - at, 0);
+    return total(x);
+  };
+  int lo = 0, hi = p.T / (2 * kTile) + 1;  // from(lo) > rank >= from(hi)
+  int above = 0;
+  if (from(0) <= rank) return false;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2, x = from(mid);
+    if (x > rank) {
+      lo = mid;
+    } else {
+      hi = mid;
+      above = x;
+    }
+  }
+  k = lo;
+  int at = rank - above;  // among the sequences with a pair k
+  for (int i0 = 0; i0 < p.B; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    const bool has = (i0 == 0 ? own : pairs(i)) > k;
+    const uint32_t votes = __ballot_sync(0xffffffffu, has);
+    const int all = total((threadIdx.x & 31) == 0 ? __popc(votes) : 0);
+    if (at < all) {
+      int before = 0;
+      for (int w = 0; w < warp; ++w) before += sums[w];
+      before += __popc(votes & ((1u << (threadIdx.x & 31)) - 1u));
+      if (has && before == at) found = i;
+      __syncthreads();
+      b = found;
+      return true;
+    }
+    at -= all;
+  }
+  return false;
 }
 
 template <int D, bool F16>
@@ -85,27 +152,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   uint64_t* empty = bars + C::NS;     // [NS] ring slot read
   uint64_t* q_full = bars + 2 * C::NS;  // [2]
   uint64_t* s_full = q_full + 2;      // [2] scores of the row tile's current key tile
-  uint64_t* p_full = q_full + 4;      // [2] its probabilities
+  uint64_t* p_full = q_full + 4;      // [2] its probabilities, first half
+  uint64_t* p_late = q_full + 12;     // [2] second half
   uint64_t* pv_done = q_full + 6;     // [2] its sums
   uint64_t* clean = q_full + 8;       // [2] values of a diagonal tile looked through
   uint64_t* sent = q_full + 10;       // [2] the copy of a diagonal tile's values is on its way
-  uint64_t* drain = q_full + 12;
+  uint64_t* drain = q_full + 14;
   uint32_t* marked = reinterpret_cast<uint32_t*>(bars + C::NBAR);  // [2][4] keys with non-finite values
   uint32_t* tmem_slot = marked + 8;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  // Blocks take the later pieces of the packed rows first: the last rows of a
-  // sequence see the most keys.
   const int head = blockIdx.x % p.H;
-  const int piece = p.pieces - 1 - static_cast<int>(blockIdx.x / p.H);
-  const int b = find_sequence(p.starts, p.B, p.T, 2 * kTile, 1, piece);
-  const int raw0 = p.starts[b], raw1 = p.starts[b + 1];
-  const int t0 = clamp_row(raw0, p.T), t1 = clamp_row(raw1, p.T);
-  if (threadIdx.x == 0 && (t0 != raw0 || t1 != raw1 || t1 < t0)) atomicOr(p.status, kStatusBadIndex);
-  const int block = piece - (t0 / (2 * kTile) + b);  // pair of row tiles of the sequence
-  const int first = block * 2 * kTile;               // its first row
+  int b, block;
+  if (!find_pair(p, static_cast<int>(blockIdx.x / p.H), b, block)) return;
+  const int t0 = clamp_row(p.starts[b], p.T), t1 = clamp_row(p.starts[b + 1], p.T);
+  const int first = block * 2 * kTile;  // the pair's first row
   const int len = t1 - t0;
-  if (block < 0 || first >= len) return;
   // Key tiles of the two row tiles; the last one of each is on its diagonal.
   const int n0 = 2 * block + 1;
   const int n1 = first + kTile < len ? n0 + 1 : 0;
@@ -125,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_init(&q_full[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
+      mbar_init(&p_late[i], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&clean[i], 2);
       mbar_init(&sent[i], 1);
@@ -224,8 +287,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           ok = wwait(&p_full[t], j & 1);
           if (!ok) break;
           tc_fence_after();
-          mma_values<D>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi), idesc_v,
-                        j > 0);
+          mma_values_half<D, 0>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi),
+                                idesc_v, j > 0);
+          ok = wwait(&p_late[t], j & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_values_half<D, 1>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi),
+                                idesc_v, true);
           umma_commit(&pv_done[t]);
           if (j + 1 < nt) scores(t, j + 1);
         }
@@ -303,6 +371,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int x = 0; x < kTile; ++x)
           if (x > row) s[x] = __float_as_uint(-INFINITY);
       }
+      // The first half's probabilities are formed at the running maximum while
+      // the row's largest score is still being found, and again only if it
+      // exceeds that maximum by more than 2^kRaise.
+      uint32_t pk[32];
+      float2 sum = make_float2(0.f, 0.f);
+      exp_half<F16>(&s[0], sc2, m, pk, sum);
       const float top = max128(s) * sc;
       if (__any_sync(0xffffffffu, top > m + kRaise)) {
         const float to = fmaxf(m, top);
@@ -310,31 +384,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         m = to;
         l *= f;
         if (j > 0) rescale_sums<D>(tO, f);
+        sum = make_float2(0.f, 0.f);
+        exp_half<F16>(&s[0], sc2, m, pk, sum);
       }
-      const float base = m == -INFINITY ? 0.f : m;
-      const float2 nb = make_float2(-base, -base);
-      float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int x = 0; x < 64; x += 4) {
-          const uint32_t* y = &s[64 * h + x];
-          float2 a = __ffma2_rn(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2, nb);
-          float2 c = __ffma2_rn(make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), sc2, nb);
-          a.x = ex2_approx(a.x), a.y = ex2_approx(a.y);
-          c.x = ex2_approx(c.x), c.y = ex2_approx(c.y);
-          sum0 = __fadd2_rn(sum0, a);
-          sum1 = __fadd2_rn(sum1, c);
-          pk[x / 2] = pack_pair<F16>(a.x, a.y);
-          pk[x / 2 + 1] = pack_pair<F16>(c.x, c.y);
-        }
-        tmem_st32(tS + 32 * h, pk);
-      }
+      tmem_st32(tS, pk);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive_if(&p_full[t], lane == 0);
-      l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+      exp_half<F16>(&s[64], sc2, m, pk, sum);
+      tmem_st32(tS + 32, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive_if(&p_late[t], lane == 0);
+      l += sum.x + sum.y;
     }
     if (ok && nt > 0 && wwait(&pv_done[t], (nt - 1) & 1) && wwait(&clean[0], 0) &&
         (t == 0 || wwait(&clean[1], 0))) {

@@ -27,16 +27,24 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
   return F16 ? Elem<__half>::pack(lo, hi) : ajvp::pack_bf16x2(lo, hi);
 }
 
-// D[tmem] (+)= P[tmem] V: P packed two keys to a column, 64 columns from
-// a_tmem on; V a [128 keys x D] tile of 64-column chunks.
+// D[tmem] (+)= P[tmem] V over one half of a tile's keys: P packed two keys to
+// a column, 64 columns from a_tmem on; V a [128 keys x D] tile of 64-column
+// chunks.
+template <int D, int HALF>
+__device__ __forceinline__ void mma_values_half(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_smem,
+                                                uint32_t idesc, bool accumulate) {
+  const uint64_t db = ajvp::smem_desc_sw128(b_smem, kTile * 128, 1024);
+#pragma unroll
+  for (int ks = 4 * HALF; ks < 4 * HALF + 4; ++ks)
+    ajvp::umma_ts(d_tmem, a_tmem + 8 * ks, db + ((ks * 16 * 128) >> 4), idesc,
+                  (accumulate || ks > 4 * HALF) ? 1u : 0u);
+}
+
 template <int D>
 __device__ __forceinline__ void mma_values(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_smem,
                                            uint32_t idesc, bool accumulate) {
-  const uint64_t db = ajvp::smem_desc_sw128(b_smem, kTile * 128, 1024);
-#pragma unroll
-  for (int ks = 0; ks < kTile / 16; ++ks)
-    ajvp::umma_ts(d_tmem, a_tmem + 8 * ks, db + ((ks * 16 * 128) >> 4), idesc,
-                  (accumulate || ks > 0) ? 1u : 0u);
+  mma_values_half<D, 0>(d_tmem, a_tmem, b_smem, idesc, accumulate);
+  mma_values_half<D, 1>(d_tmem, a_tmem, b_smem, idesc, true);
 }
 
 // 3-D tiled load, as tma_load_4d_hint.
@@ -85,6 +93,27 @@ __device__ __forceinline__ float max128(const uint32_t (&s)[kTile]) {
     for (int i = 0; i < 4; ++i)
       m[i] = ajvp::fmax3(m[i], __uint_as_float(s[j + 2 * i]), __uint_as_float(s[j + 2 * i + 1]));
   return fmaxf(ajvp::fmax3(m[0], m[1], m[2]), m[3]);
+}
+
+// 2^(s * sc - m) of 64 scores, packed in pairs, and their sum added to `sum`.
+template <bool F16>
+__device__ __forceinline__ void exp_half(const uint32_t* s, float2 sc, float m, uint32_t (&pk)[32],
+                                         float2& sum) {
+  const float base = m == -INFINITY ? 0.f : m;
+  const float2 nb = make_float2(-base, -base);
+  float2 other = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int x = 0; x < 64; x += 4) {
+    float2 a = __ffma2_rn(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), sc, nb);
+    float2 c = __ffma2_rn(make_float2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), sc, nb);
+    a.x = ajvp::ex2_approx(a.x), a.y = ajvp::ex2_approx(a.y);
+    c.x = ajvp::ex2_approx(c.x), c.y = ajvp::ex2_approx(c.y);
+    sum = __fadd2_rn(sum, a);
+    other = __fadd2_rn(other, c);
+    pk[x / 2] = pack_pair<F16>(a.x, a.y);
+    pk[x / 2 + 1] = pack_pair<F16>(c.x, c.y);
+  }
+  sum = __fadd2_rn(sum, other);
 }
 
 }  // namespace ajvp_serve
