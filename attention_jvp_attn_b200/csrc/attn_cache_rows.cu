@@ -10,52 +10,74 @@
 // so p is at most 2^kLazyMax however the scales differ, and what fp16 rounds
 // away of p is small against the largest contribution to O.
 //
-// Bound by HBM: a cached token is 2 d bytes per key head, read once; 16 rows
+// Bound by HBM: a cached token is 2 d bytes per key head, read once; the rows
 // (all query heads of the key head, and the newest tokens) share it. Codes are
 // exact in fp16, so both products run on m16n8k16 fp16 matrix instructions
 // with fp32 sums; bf16 queries are scaled by a power of two per row into fp16
 // (exact within 2^-14 of the row's largest, absolute error 2^-25 of it below).
-// 128-row tensor-memory tiles would leave 7/8 of the rows unused here.
+// Tokens are the instruction's 16 rows and query rows its 8 columns
+// (S^T = K Q^T, O^T = V^T P^T), so 8 query rows cost no padding and each code
+// is converted once however many query rows there are; 128-row tensor-memory
+// tiles would be mostly empty here.
 //
 // Layout: each warp streams its own steps of 32 tokens through a private ring
-// of asynchronous copies (no block-wide barrier in the loop), so a stall of
-// one warp holds up no other. The order of the head dimension inside the
-// products is free, so a lane takes 16 adjacent codes at a time for four
-// matrix instructions, and the column order of O lets a lane own adjacent
-// columns: no shared-memory transposes. The key axis of one tile is split
-// over the blocks of a cluster, which join their sums through distributed
-// shared memory: one launch, no workspace, a fixed order of sums.
+// of TMA copies (no block-wide barrier in the loop), so a stall of one warp
+// holds up no other. The order of the head dimension inside the products is
+// free, so a lane takes 16 adjacent codes at a time for four matrix
+// instructions, and the column order of O lets a lane own adjacent columns: no
+// shared-memory transposes. The key axis of one tile is split over the blocks
+// of a cluster, which join their sums through distributed shared memory: one
+// launch, no workspace, a fixed order of sums.
+#include <cuda.h>
+
 #include "serve_attn.cuh"
 
 #include <type_traits>
 
 namespace ajvp_serve {
 
+namespace {
+
 constexpr int kRowsWarps = 4;
-constexpr int kStep = 32;  // tokens per step of a warp
+constexpr int kStep = 32;                  // tokens per step of a warp
 constexpr uint32_t kHidden = 0xffffffffu;  // in place of a key scale: no page there
 
-template <int D>
-struct RowsCfg {
-  static constexpr int STAGES = D == 128 ? 3 : 4;
-  static constexpr int KV = kStep * D;            // bytes of a step's keys (or values)
-  static constexpr int STAGE = 2 * KV + 16;       // and k, v scales of its two 16-token halves
-  static constexpr int RING = STAGES * STAGE;     // per warp
-  static constexpr int PART = kRowsTile * D * 4;  // one warp's sums
-  static constexpr int BYTES = kRowsWarps * (RING > PART ? RING : PART) + PART + 3 * 4 * kRowsTile * kRowsWarps;
+struct RowsParams {
+  CUtensorMap map_k, map_v;  // codes (d, page tokens, heads, pages), boxes of d x box tokens
+  CacheAttnParams c;
+  int box;  // 16 or 32 tokens, one page's
 };
 
-// Where 16-byte chunk q of token row r lies in a step's keys or values, so
-// that the lanes of a quarter warp hit all banks: they read 2 rows x 4 chunks
-// of the keys, 4 even rows x 2 chunks of the values.
+template <int D, int NT>
+struct RowsCfg {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int STAGES = 3;
+  static constexpr int KV = kStep * D;                // bytes of a step's keys (or values)
+  static constexpr int RING = STAGES * 2 * KV;        // per warp
+  static constexpr int PITCH = D + 4;                 // floats per row of a warp's sums
+  static constexpr int PART = ROWS * PITCH * 4;
+  static constexpr int SLOT = RING;                   // the sums lie over the ring
+  static constexpr int SCALES = STAGES * 4 * 4;       // per warp: k, v scales of the 16-token halves
+  static constexpr int AT_WHOLE = kRowsWarps * SLOT;  // the block's sums
+  static constexpr int AT_STATS = AT_WHOLE + PART;
+  static constexpr int AT_SCALES = AT_STATS + (2 * kRowsWarps + 2) * ROWS * 4;
+  static constexpr int AT_BARS = AT_SCALES + kRowsWarps * SCALES;
+  static constexpr int BYTES = 1024 + AT_BARS + kRowsWarps * STAGES * 8 + 16;
+  static_assert(PART <= SLOT && SLOT % 1024 == 0 && AT_BARS % 8 == 0, "layout");
+};
+
+// A lane's place in the instruction: g = lane / 4 its token (or column of O),
+// c = lane % 4 its columns (or tokens). Which tokens and which 16 codes those
+// stand for is free, and chosen so that the eight lanes of a shared-memory
+// phase hit all banks of the TMA-swizzled rows (128-byte swizzle for d = 128,
+// 64-byte for d = 64).
 template <int D>
-__device__ __forceinline__ int k_place(int r, int q) {
-  return D == 128 ? r * 128 + ((q ^ ((r & 1) << 2)) << 4) : r * 64 + (q << 4);
+__device__ __forceinline__ int token_of(int g) {  // of row g of the instruction's first 8
+  return D == 128 ? (g >> 1) | ((g & 1) << 2) : g ^ ((g >> 1) & 1);
 }
 template <int D>
-__device__ __forceinline__ int v_place(int r, int q) {
-  return D == 128 ? r * 128 + ((q ^ (((r >> 1) & 3) << 1)) << 4)
-                  : (r >> 1) * 128 + (((((r & 1) << 2) + q) ^ (((r >> 1) & 3) << 1)) << 4);
+__device__ __forceinline__ int place(int r, int q) {  // 16-byte chunk q of token row r
+  return D == 128 ? r * 128 + ((q ^ (r & 7)) << 4) : r * 64 + ((q ^ ((r >> 1) & 3)) << 4);
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -67,46 +89,107 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  return Elem<__half>::pack(a, b);
+// Transpose of an 8 x 8 matrix of 16-bit values held two to a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __grid_constant__ CacheAttnParams p) {
-  using C = RowsCfg<D>;
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) { return Elem<__half>::pack(a, b); }
+
+__device__ __forceinline__ uint32_t lo16(uint32_t w) { return e4m3x2_to_f16x2(w & 0xffffu); }
+__device__ __forceinline__ uint32_t hi16(uint32_t w) { return e4m3x2_to_f16x2(w >> 16); }
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __grid_constant__ RowsParams params) {
+  using C = RowsCfg<D, NT>;
+  const CacheAttnParams& p = params.c;
   constexpr int H2 = D / 64;  // 64-column parts of the head dimension
-  constexpr int VB = D / 8;   // output columns (value bytes) per lane and row
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int VB = D / 8;   // output columns (value bytes) per lane
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::AT_BARS) + warp * C::STAGES;
+  volatile int* abort_flag =
+      reinterpret_cast<volatile int*>(smem + C::AT_BARS + kRowsWarps * C::STAGES * 8);
 
   const int tile = blockIdx.x / p.splits, rank = blockIdx.x - tile * p.splits;
   const int rt = tile % p.row_tiles, bh = tile / p.row_tiles;
   const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
   const int rows = p.n * p.group;  // rows of this key head: token-major, then head of the group
-  const int row0 = rt * kRowsTile;
+  const int row0 = rt * C::ROWS;
   const int len = checked_len(p, b);
-
-  // This lane's rows g and g + 8: keys they see.
-  int seen[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = min(row0 + g + 8 * i, rows - 1);
-    seen[i] = p.causal ? max(len - p.n + r / p.group + 1, 0) : len;
+  if (threadIdx.x == 0) *abort_flag = 0;
+  if (lane == 0) {
+    for (int i = 0; i < C::STAGES; ++i) ajvp::mbar_init(&full[i], 1);
+    ajvp::fence_barrier_init();
   }
-  const int last = min(row0 + kRowsTile, rows) - 1;
-  const int reach = p.causal ? max(len - p.n + last / p.group + 1, 0) : len;   // most keys seen
-  const int all = p.causal ? max(len - p.n + row0 / p.group + 1, 0) : len;     // keys all rows see
+  __syncthreads();
+
+  const int last = min(row0 + C::ROWS, rows) - 1;
+  const int reach = p.causal ? max(len - p.n + last / p.group + 1, 0) : len;  // most keys seen
+  const int all = p.causal ? max(len - p.n + row0 / p.group + 1, 0) : len;    // keys all rows see
   const int steps = (reach + kStep - 1) / kStep;
   const int s_begin = static_cast<int>(int64_t(steps) * rank / p.splits);
   const int s_end = static_cast<int>(int64_t(steps) * (rank + 1) / p.splits);
 
-  // Queries as fp16 fragments: k-step (h, s) holds columns (c + 4h) 16 + 4s + 0..3.
-  uint32_t q[H2][4][4];
-  float row_scale[2];
+  uint8_t* ring = smem + warp * C::SLOT;
+  float* scales = reinterpret_cast<float*>(smem + C::AT_SCALES + warp * C::SCALES);
+
+  // Pages of step s: lanes 0 and 1 those of its 16-token halves; -1: none.
+  auto page_of = [&](int s) -> int {
+    const int j = s * kStep + (lane & 1) * 16;
+    return lane < 2 && s < s_end && j < reach ? checked_page(p, b, j) : -1;
+  };
+  // Copies step s, whose pages are `page`, into stage st. Returns what lanes
+  // 0 to 3 will put into the stage's scales: keys (0, 1) and values (2, 3) of
+  // the halves, a mark for a hidden half's keys.
+  int issued = 0, taken = 0;  // steps whose copies were issued, and waited for
+  auto fetch = [&](int s, int st, int page) -> float {
+    const int page0 = __shfl_sync(0xffffffffu, page, 0), page1 = __shfl_sync(0xffffffffu, page, 1);
+    float sc = lane < 2 ? __uint_as_float(kHidden) : 1.f;
+    if (s < s_end) {
+      ++issued;
+      uint8_t* at = ring + st * 2 * C::KV;
+      const int j = (s * kStep) & ((1 << p.page_shift) - 1);
+      if (lane == 0) {
+        const int boxes = params.box == kStep ? (page0 >= 0) : (page0 >= 0) + (page1 >= 0);
+        ajvp::mbar_arrive_expect_tx(&full[st], boxes * params.box * D * 2);
+        if (page0 >= 0) {
+          ajvp::tma_load_4d(at, &params.map_k, &full[st], 0, j, hk, page0);
+          ajvp::tma_load_4d(at + C::KV, &params.map_v, &full[st], 0, j, hk, page0);
+        }
+        if (params.box != kStep && page1 >= 0) {
+          ajvp::tma_load_4d(at + 16 * D, &params.map_k, &full[st], 0, 0, hk, page1);
+          ajvp::tma_load_4d(at + C::KV + 16 * D, &params.map_v, &full[st], 0, 0, hk, page1);
+        }
+      }
+      const int pg = (lane & 1) ? page1 : page0;
+      if (lane < 4 && pg >= 0) sc = p.scale[lane >> 1][pg * p.scale_page + hk * p.scale_head];
+    }
+    return sc;
+  };
+
+  int next = s_begin + warp;  // next step to copy
+  int page = page_of(next);
+  float pending = 0.f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = row0 + g + 8 * i;
+  for (int i = 0; i < C::STAGES - 1; ++i) {
+    pending = fetch(next, i, page);
+    next += kRowsWarps;
+    page = page_of(next);
+    if (lane < 4) scales[4 * i + lane] = pending;
+  }
+
+  // Queries as fp16 fragments: k-step (h, s) holds columns (c + 4h) 16 + 4s + 0..3 of row g.
+  uint32_t q[NT][H2][4][2];
+  float row_scale[NT][2];  // of rows 2c, 2c + 1
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = row0 + 8 * t + g;
     float x[H2][16];
     float amax = 0.f;
     const int token = r / p.group, head = hk * p.group + r - token * p.group;
@@ -129,187 +212,168 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
         }
       }
     }
-    float inv = 1.f;
-    row_scale[i] = p.scale_log2;
-    if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+    float inv = 1.f, mine = p.scale_log2;
+    if constexpr (!std::is_same<T, __half>::value) {
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       int e = 0;
       if (amax > 0.f) frexpf(amax, &e);
       e = min(max(e, -100), 100);
       inv = ldexpf(1.f, -e);
-      row_scale[i] *= ldexpf(1.f, e);
+      mine *= ldexpf(1.f, e);
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) row_scale[t][i] = __shfl_sync(0xffffffffu, mine, 4 * (2 * c + i));
 #pragma unroll
     for (int h = 0; h < H2; ++h)
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        q[h][s][i] = pack_f16(x[h][4 * s] * inv, x[h][4 * s + 1] * inv);
-        q[h][s][2 + i] = pack_f16(x[h][4 * s + 2] * inv, x[h][4 * s + 3] * inv);
+        q[t][h][s][0] = pack_f16(x[h][4 * s] * inv, x[h][4 * s + 1] * inv);
+        q[t][h][s][1] = pack_f16(x[h][4 * s + 2] * inv, x[h][4 * s + 3] * inv);
       }
   }
-
-  uint8_t* ring = smem + warp * (C::RING > C::PART ? C::RING : C::PART);
-  const uint32_t ring_addr = ajvp::smem_u32(ring);
-  const uint8_t* kb = p.codes[0] + hk * p.head_stride;
-  const uint8_t* vb = p.codes[1] + hk * p.head_stride;
-  const int in_page = (1 << p.page_shift) - 1;
-
-  // The page of this lane's 16-token half (lane / 16) of step s; -1: none.
-  auto page_of = [&](int s) -> int {
-    const int j = s * kStep + (lane & 16);
-    return s < s_end && j < reach ? checked_page(p, b, j) : -1;
-  };
-  // Copies step s, whose pages are `page`, into stage st.
-  auto fetch = [&](int s, int st, int page) {
-    if (s < s_end) {
-      const uint32_t at = ring_addr + st * C::STAGE;
-      constexpr int Q = D / 16, PER = 32 / Q;  // chunks of a row, rows per round of the warp
-      const int chunk = lane % Q, first = lane / Q;
+  int seen[NT][2];  // keys that rows 2c, 2c + 1 see
 #pragma unroll
-      for (int i = 0; i < kStep / PER; ++i) {
-        const int r = first + i * PER;
-        const int j = s * kStep + r;
-        const int pg = __shfl_sync(0xffffffffu, page, r & 16);
-        const bool valid = pg >= 0 && j < reach;
-        const int64_t off = valid ? pg * p.page_stride + (j & in_page) * p.token_stride + chunk * 16 : 0;
-        copy16(at + k_place<D>(r, chunk), kb + off, valid);
-        copy16(at + C::KV + v_place<D>(r, chunk), vb + off, valid);
-      }
-      // scales of the halves: lanes 0, 16 keys, 1, 17 values; a hidden half has the mark
-      if ((lane & 15) < 2) {
-        float* dst = reinterpret_cast<float*>(ring + st * C::STAGE + 2 * C::KV) + (lane & 1) * 2 + (lane >> 4);
-        if (page >= 0) {
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ajvp::smem_u32(dst)),
-                       "l"(p.scale[lane & 1] + page * p.scale_page + hk * p.scale_head)
-                       : "memory");
-        } else {
-          *dst = (lane & 1) ? 1.f : __uint_as_float(kHidden);
-        }
-      }
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = min(row0 + 8 * t + 2 * c + i, rows - 1);
+      seen[t][i] = p.causal ? max(len - p.n + r / p.group + 1, 0) : len;
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
 
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float acc[VB][4];
+  float m[NT][2], l[NT][2], acc[NT][VB / 2][4];
 #pragma unroll
-  for (int j = 0; j < VB; ++j)
+  for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    for (int i = 0; i < 2; ++i) m[t][i] = -INFINITY, l[t][i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < VB / 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][j][i] = 0.f;
+  }
 
-  int next = s_begin + warp;  // next step to copy
-  int page = page_of(next);
-#pragma unroll
-  for (int i = 0; i < C::STAGES - 1; ++i) {
-    fetch(next, i, page);
+  int stage = 0, into = C::STAGES - 1;
+  uint32_t phase = 0;
+  bool late = false;  // `pending` belongs to the stage before `into`
+  __syncwarp();
+  for (int s = s_begin + warp; s < s_end; s += kRowsWarps) {
+    if (late && lane < 4) scales[4 * (into == 0 ? C::STAGES - 1 : into - 1) + lane] = pending;
+    // the stage's reads are over since the end of the last round
+    pending = fetch(next, into, page);
+    late = true;
     next += kRowsWarps;
     page = page_of(next);
-  }
-  int stage = 0;
-  for (int s = s_begin + warp; s < s_end; s += kRowsWarps) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 2) : "memory");
+    if (++into == C::STAGES) into = 0;
+    if (!ajvp::warp_wait(&full[stage], phase, abort_flag, p.status)) break;
+    ++taken;
     __syncwarp();
-    {
-      int into = stage + C::STAGES - 1;
-      if (into >= C::STAGES) into -= C::STAGES;
-      fetch(next, into, page);
-      next += kRowsWarps;
-      page = page_of(next);
-    }
-    const uint8_t* sk = ring + stage * C::STAGE;
+    const uint8_t* sk = ring + stage * 2 * C::KV;
     const uint8_t* sv = sk + C::KV;
-    const float* ss = reinterpret_cast<const float*>(sv + C::KV);
-    float t[4][4];  // 8-token tiles: rows g (0, 1), g + 8 (2, 3), tokens 8 i + 2c, + 1
+    const float4 ss = *reinterpret_cast<const float4*>(scales + 4 * stage);
+
+    float x[NT][2][4];  // 16-token halves: token g (0, 1) and g + 8 (2, 3), rows 2c (0, 2), 2c + 1
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      t[i][0] = t[i][1] = t[i][2] = t[i][3] = 0.f;
+    for (int f = 0; f < 2; ++f) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) x[t][f][0] = x[t][f][1] = x[t][f][2] = x[t][f][3] = 0.f;
+      const int r = 16 * f + token_of<D>(g);
 #pragma unroll
       for (int h = 0; h < H2; ++h) {
-        const uint4 w = *reinterpret_cast<const uint4*>(sk + k_place<D>(8 * i + g, c + 4 * h));
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        const uint4 u = *reinterpret_cast<const uint4*>(sk + place<D>(r, c + 4 * h));
+        const uint4 w = *reinterpret_cast<const uint4*>(sk + place<D>(r + 8, c + 4 * h));
+        const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma_f16(t[i], q[h][e][0], q[h][e][1], q[h][e][2], q[h][e][3],
-                  e4m3x2_to_f16x2(ws[e] & 0xffffu), e4m3x2_to_f16x2(ws[e] >> 16));
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t a0 = lo16(us[e]), a1 = lo16(ws[e]), a2 = hi16(us[e]), a3 = hi16(ws[e]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_f16(x[t][f], a0, a1, a2, a3, q[t][h][e][0], q[t][h][e][1]);
+        }
       }
     }
     // scores in powers of two, the value scale in the exponent
-    float inv_v[2];
+    const bool hidden[2] = {__float_as_uint(ss.x) == kHidden, __float_as_uint(ss.y) == kHidden};
+    const float ks[2] = {read_scale(ss.x), read_scale(ss.y)};
+    const float vs[2] = {read_scale(ss.z), read_scale(ss.w)};
+    const float lv[2] = {log2_approx(vs[0]), log2_approx(vs[1])};
     const int j0 = s * kStep;
-    const bool edge = j0 + kStep > all;
-    float top[2] = {-INFINITY, -INFINITY};
+    const bool edge = j0 + kStep > all || hidden[0] || hidden[1];
+    float top[NT][2];
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const float ks = ss[f], vs = read_scale(ss[2 + f]);
-      inv_v[f] = 1.f / vs;
-      const float lv = log2_approx(vs);
-      const bool none = __float_as_uint(ks) == kHidden;
-      const float kr = read_scale(ks);
-      const float a[2] = {row_scale[0] * kr, row_scale[1] * kr};
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int i = 2 * f; i < 2 * f + 2; ++i)
+      for (int f = 0; f < 2; ++f)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = fmaf(t[i][e], a[e >> 1], lv);
-          if (none || (edge && j0 + 8 * i + 2 * c + (e & 1) >= seen[e >> 1])) x = -INFINITY;
-          t[i][e] = x;
-          top[e >> 1] = fmaxf(top[e >> 1], x);
-        }
-    }
+        for (int e = 0; e < 4; ++e)
+          x[t][f][e] = fmaf(x[t][f][e], row_scale[t][e & 1] * ks[f], lv[f]);
+      if (edge) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-    }
-    if (__any_sync(0xffffffffu, top[0] > m[0] + kLazyMax || top[1] > m[1] + kLazyMax)) {
+        for (int f = 0; f < 2; ++f)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float to = fmaxf(m[i], top[i]);
-        const float f = to == -INFINITY ? 1.f : ajvp::ex2_approx(m[i] - to);
-        m[i] = to;
-        l[i] *= f;
-#pragma unroll
-        for (int j = 0; j < VB; ++j) {
-          acc[j][2 * i] *= f;
-          acc[j][2 * i + 1] *= f;
-        }
+          for (int e = 0; e < 4; ++e)
+            if (hidden[f] || j0 + 16 * f + token_of<D>(g) + 8 * (e >> 1) >= seen[t][e & 1])
+              x[t][f][e] = -INFINITY;
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        top[t][i] = fmaxf(fmaxf(x[t][0][i], x[t][0][i + 2]), fmaxf(x[t][1][i], x[t][1][i + 2]));
     }
-    const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+    bool raise = false;
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      float sum[2] = {0.f, 0.f};
-      uint32_t seen_pairs[4] = {0, 0, 0, 0};  // 1.0 where a row sees the token (the slow path below)
-      uint32_t pk[4];
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float (&x)[4] = t[2 * f + i];
+      for (int i = 0; i < 2; ++i) raise |= top[t][i] > m[t][i] + kLazyMax;
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float to = top[t][i];
+          to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 4));
+          to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 8));
+          to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 16));
+          to = fmaxf(to, m[t][i]);
+          const float f = to == -INFINITY ? 1.f : ajvp::ex2_approx(m[t][i] - to);
+          m[t][i] = to;
+          l[t][i] *= f;
+#pragma unroll
+          for (int j = 0; j < VB / 2; ++j) {
+            acc[t][j][i] *= f;
+            acc[t][j][2 + i] *= f;
+          }
+        }
+    }
+    uint32_t pk[NT][2][2], vis[NT][2][2];  // probabilities, and 1.0 where a row sees a token
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float base[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const float inv_v = 1.f / vs[f];
         if (edge) {
-          seen_pairs[2 * i] = pack_f16(x[0] != -INFINITY, x[1] != -INFINITY);
-          seen_pairs[2 * i + 1] = pack_f16(x[2] != -INFINITY, x[3] != -INFINITY);
+          vis[t][f][0] = transpose8(pack_f16(x[t][f][0] != -INFINITY, x[t][f][1] != -INFINITY));
+          vis[t][f][1] = transpose8(pack_f16(x[t][f][2] != -INFINITY, x[t][f][3] != -INFINITY));
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = ajvp::ex2_approx(x[e] - base[e >> 1]);
-          sum[e >> 1] += x[e];
-        }
-        pk[2 * i] = pack_f16(x[0], x[1]);
-        pk[2 * i + 1] = pack_f16(x[2], x[3]);
+        for (int e = 0; e < 4; ++e) x[t][f][e] = ajvp::ex2_approx(x[t][f][e] - base[e & 1]);
+        l[t][0] = fmaf(x[t][f][0] + x[t][f][2], inv_v, l[t][0]);
+        l[t][1] = fmaf(x[t][f][1] + x[t][f][3], inv_v, l[t][1]);
+        pk[t][f][0] = transpose8(pack_f16(x[t][f][0], x[t][f][1]));
+        pk[t][f][1] = transpose8(pack_f16(x[t][f][2], x[t][f][3]));
       }
-      l[0] = fmaf(sum[0], inv_v[f], l[0]);
-      l[1] = fmaf(sum[1], inv_v[f], l[1]);
-      // values of tokens 2c, 2c + 1, 2c + 8, 2c + 9, columns VB g .. + VB
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      // values of the instruction's tokens 2c, 2c + 1, 2c + 8, 2c + 9, the lane's columns
       uint32_t w[4][VB / 4];
       bool nan = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = 16 * f + 2 * c + (i & 1) + 8 * (i >> 1);
+        const int r = 16 * f + token_of<D>(2 * c + (i & 1)) + 8 * (i >> 1);
         if constexpr (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sv + v_place<D>(r, g));
+          const uint4 u = *reinterpret_cast<const uint4*>(sv + place<D>(r, token_of<D>(g)));
           w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
         } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(sv + v_place<D>(r, g >> 1) + 8 * (g & 1));
+          const uint2 u = *reinterpret_cast<const uint2*>(sv + place<D>(r, g >> 1) + 8 * (g & 1));
           w[i][0] = u.x, w[i][1] = u.y;
         }
         if (edge) {
@@ -318,169 +382,173 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
             nan |= (((w[i][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
         }
       }
-      // A NaN value where some rows see the token and some do not: it must not
-      // reach the rows that do not (0 * NaN). It is taken out of the product,
-      // and a second product, of what each row sees and where the NaN are,
-      // says which sums become NaN.
+      // A NaN value where some rows see the token and some do not (or none: what
+      // an earlier owner of the page left there): it must not reach the rows
+      // that do not (0 * NaN). It is taken out of the product, and a second
+      // product, of what each row sees and where the NaN are, says which sums
+      // become NaN.
       const bool apart = edge && __any_sync(0xffffffffu, nan);
 #pragma unroll
-      for (int e = 0; e < VB / 4; ++e) {
+      for (int e = 0; e < VB / 4; ++e)
 #pragma unroll
         for (int hi = 0; hi < 2; ++hi) {
           // bytes 2hi, 2hi + 1 of the two tokens of a pair, interleaved
           const uint32_t sel = hi ? 0x7362u : 0x5140u;
           uint32_t p0 = __byte_perm(w[0][e], w[1][e], sel), p1 = __byte_perm(w[2][e], w[3][e], sel);
+          const int j = 2 * e + hi;
           if (apart) {
             const uint32_t n0 = (((p0 & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
             const uint32_t n1 = (((p1 & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
             p0 &= ~(n0 * 0xffu);
             p1 &= ~(n1 * 0xffu);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int t = 0; t < NT; ++t) {
               float hit[4] = {0.f, 0.f, 0.f, 0.f};
               // 0x38 is the e4m3 code of 1
-              mma_f16(hit, seen_pairs[0], seen_pairs[1], seen_pairs[2], seen_pairs[3],
-                      e4m3x2_to_f16x2(((n0 * 0x38u) >> (16 * k)) & 0xffffu),
-                      e4m3x2_to_f16x2(((n1 * 0x38u) >> (16 * k)) & 0xffffu));
+              mma_f16(hit, lo16(n0 * 0x38u), hi16(n0 * 0x38u), lo16(n1 * 0x38u), hi16(n1 * 0x38u),
+                      vis[t][f][0], vis[t][f][1]);
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (hit[x] > 0.f) acc[4 * e + 2 * hi + k][x] = NAN;
+              for (int i = 0; i < 4; ++i)
+                if (hit[i] > 0.f) acc[t][j][i] = NAN;
             }
           }
+          const uint32_t a0 = lo16(p0), a1 = hi16(p0), a2 = lo16(p1), a3 = hi16(p1);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            mma_f16(acc[4 * e + 2 * hi + k], pk[0], pk[1], pk[2], pk[3],
-                    e4m3x2_to_f16x2((p0 >> (16 * k)) & 0xffffu),
-                    e4m3x2_to_f16x2((p1 >> (16 * k)) & 0xffffu));
+          for (int t = 0; t < NT; ++t) mma_f16(acc[t][j], a0, a1, a2, a3, pk[t][f][0], pk[t][f][1]);
         }
-      }
     }
     __syncwarp();
-    if (++stage == C::STAGES) stage = 0;
+    if (++stage == C::STAGES) stage = 0, phase ^= 1;
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  // After an abort copies may still be on their way: they land before the ring
+  // is written over. (A normal end has waited for each.)
+  for (; taken < issued; ++taken)
+    ajvp::mbar_wait_drain(&full[taken % C::STAGES], (taken / C::STAGES) & 1, 200000000ull);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-  }
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 4);
+      l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 8);
+      l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 16);
+    }
 
   // Join the warps: each leaves its sums in its ring, then the block adds them
   // up into `whole`, and the cluster's blocks add those up.
-  constexpr int SLOT = C::RING > C::PART ? C::RING : C::PART;
-  float* whole = reinterpret_cast<float*>(smem + kRowsWarps * SLOT);
-  float* wm = whole + kRowsTile * D;              // [warps][16]: running maxima
-  float* wl = wm + kRowsTile * kRowsWarps;        // [warps][16]: sums
-  float* bm = wl + kRowsTile * kRowsWarps;        // [16]: the block's maxima, then [16] sums
+  float* whole = reinterpret_cast<float*>(smem + C::AT_WHOLE);
+  float* wm = reinterpret_cast<float*>(smem + C::AT_STATS);  // [warps][ROWS]: running maxima
+  float* wl = wm + C::ROWS * kRowsWarps;                     // [warps][ROWS]: sums
+  float* bm = wl + C::ROWS * kRowsWarps;                     // [ROWS]: the block's maxima, then sums
   __syncwarp();
   {
     float* part = reinterpret_cast<float*>(ring);
+    const int col = D == 128 ? token_of<D>(g) * VB : g * VB;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int j = 0; j < VB; j += 4)
-          *reinterpret_cast<float4*>(part + (g + 8 * i) * D + (2 * c + u) * VB + j) =
-              make_float4(acc[j][2 * i + u], acc[j + 1][2 * i + u], acc[j + 2][2 * i + u],
-                          acc[j + 3][2 * i + u]);
-    if (c == 0) {
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        wm[warp * kRowsTile + g + 8 * i] = m[i];
-        wl[warp * kRowsTile + g + 8 * i] = l[i];
+        const int r = 8 * t + 2 * c + i;
+#pragma unroll
+        for (int j = 0; j < VB / 2; j += 2)
+          *reinterpret_cast<float4*>(part + r * C::PITCH + col + 2 * j) =
+              make_float4(acc[t][j][i], acc[t][j][2 + i], acc[t][j + 1][i], acc[t][j + 1][2 + i]);
+        if (g == 0) {
+          wm[warp * C::ROWS + r] = m[t][i];
+          wl[warp * C::ROWS + r] = l[t][i];
+        }
       }
-    }
   }
   __syncthreads();
-  constexpr int TPR = kRowsWarps * 32 / kRowsTile;  // threads per row
-  const int jr = threadIdx.x / TPR, jc = threadIdx.x % TPR;
-  {
+  constexpr int kThreads = kRowsWarps * 32;
+  for (int item = threadIdx.x; item < C::ROWS * (D / 4); item += kThreads) {
+    const int r = item / (D / 4), col = (item % (D / 4)) * 4;
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, wm[w * kRowsTile + jr]);
-    float f[kRowsWarps], sum = 0.f;
+    for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, wm[w * C::ROWS + r]);
+    float sum = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kRowsWarps; ++w) {
-      f[w] = top == -INFINITY ? 0.f : ajvp::ex2_approx(wm[w * kRowsTile + jr] - top);
       // a warp that saw no key has sum 0 and maximum -inf; NaN sums pass on
-      sum += wl[w * kRowsTile + jr] * f[w];
+      const float f = top == -INFINITY ? 1.f : ajvp::ex2_approx(wm[w * C::ROWS + r] - top);
+      sum = fmaf(wl[w * C::ROWS + r], f, sum);
+      const float4 z = *reinterpret_cast<const float4*>(smem + w * C::SLOT + (r * C::PITCH + col) * 4);
+      y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y);
+      y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
     }
-    for (int x = jc * 4; x < D; x += TPR * 4) {
-      float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kRowsWarps; ++w) {
-        const float4 y = *reinterpret_cast<const float4*>(smem + w * SLOT + (jr * D + x) * 4);
-        r.x = fmaf(y.x, f[w], r.x), r.y = fmaf(y.y, f[w], r.y);
-        r.z = fmaf(y.z, f[w], r.z), r.w = fmaf(y.w, f[w], r.w);
-      }
-      *reinterpret_cast<float4*>(whole + jr * D + x) = r;
-    }
-    if (jc == 0) {
-      bm[jr] = top;
-      bm[kRowsTile + jr] = sum;
-    }
+    *reinterpret_cast<float4*>(whole + r * C::PITCH + col) = y;
+    if (col == 0) bm[r] = top, bm[C::ROWS + r] = sum;
   }
   if (p.splits > 1)
     ajvp::cluster_sync_all();
   else
     __syncthreads();
 
-  // Rank r of the cluster joins and writes rows r, r + splits, ...
+  // Block `rank` of the cluster joins and writes every splits-th group of 4 columns.
   const uint32_t whole_addr = ajvp::smem_u32(whole), bm_addr = ajvp::smem_u32(bm);
-  for (int item = threadIdx.x; item < kRowsTile * (D / 8); item += kRowsWarps * 32) {
-    const int r = (item / (D / 8)) * 1, x = (item % (D / 8)) * 8;
+  for (int item = rank + threadIdx.x * p.splits; item < C::ROWS * (D / 4); item += kThreads * p.splits) {
+    const int r = item / (D / 4), col = (item % (D / 4)) * 4;
     const int row = row0 + r;
-    if (r % p.splits != rank || row >= rows) continue;
-    float top = -INFINITY, sum = 0.f, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (row >= rows) continue;
+    float top = -INFINITY, sum = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < p.splits; ++k)
       top = fmaxf(top, ld_cluster_f32(ajvp::mapa_shared(bm_addr + r * 4, k)));
     for (int k = 0; k < p.splits; ++k) {
       const float mk = ld_cluster_f32(ajvp::mapa_shared(bm_addr + r * 4, k));
-      const float f = top == -INFINITY ? 0.f : ajvp::ex2_approx(mk - top);
-      sum = fmaf(ld_cluster_f32(ajvp::mapa_shared(bm_addr + (kRowsTile + r) * 4, k)), f, sum);
-      const uint32_t at = ajvp::mapa_shared(whole_addr + (r * D + x) * 4, k);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = fmaf(ld_cluster_f32(at + 4 * e), f, y[e]);
+      const float f = top == -INFINITY ? 1.f : ajvp::ex2_approx(mk - top);
+      sum = fmaf(ld_cluster_f32(ajvp::mapa_shared(bm_addr + (C::ROWS + r) * 4, k)), f, sum);
+      const float4 z = ld_cluster_f32x4(ajvp::mapa_shared(whole_addr + (r * C::PITCH + col) * 4, k));
+      y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y);
+      y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
     }
     const int token = row / p.group, head = hk * p.group + row - token * p.group;
-    const float inv = top == -INFINITY && sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] *= inv;
-    T* dst = static_cast<T*>(p.o) + ((int64_t(b) * p.n + token) * p.H + head) * D + x;
-    store8(dst, y);
-    if (x == 0)
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen (a NaN sum is not 0)
+    T* dst = static_cast<T*>(p.o) + ((int64_t(b) * p.n + token) * p.H + head) * D + col;
+    uint2 u;
+    u.x = Elem<T>::pack(y.x * inv, y.y * inv);
+    u.y = Elem<T>::pack(y.z * inv, y.w * inv);
+    *reinterpret_cast<uint2*>(dst) = u;
+    if (col == 0)
       p.lse[(int64_t(b) * p.H + head) * p.n + token] =
-          top == -INFINITY && sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+          sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
   if (p.splits > 1) ajvp::cluster_sync_all();  // no block leaves while its sums are read
 }
 
-template <typename T, int D>
-cudaError_t rows_launch(const CacheAttnParams& p, cudaStream_t st) {
-  using C = RowsCfg<D>;
+template <typename T, int D, int NT>
+cudaError_t rows_launch(const RowsParams& p, cudaStream_t st) {
+  using C = RowsCfg<D, NT>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(cache_rows_kernel<T, D>, C::BYTES, done);
+  const cudaError_t e = allow_smem(cache_rows_kernel<T, D, NT>, C::BYTES, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.row_tiles * p.splits));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.c.B * p.c.Hkv * p.c.row_tiles * p.c.splits));
   cfg.blockDim = dim3(kRowsWarps * 32);
   cfg.dynamicSmemBytes = C::BYTES;
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.splits;
+  attr.val.clusterDim.x = p.c.splits;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_rows_kernel<T, D>, p);
+  return cudaLaunchKernelEx(&cfg, cache_rows_kernel<T, D, NT>, p);
 }
 
-cudaError_t cache_rows_launch(const CacheAttnParams& p, int d, int dtype, cudaStream_t st) {
+template <typename T, int D>
+cudaError_t rows_launch(const RowsParams& p, cudaStream_t st) {
+  return p.c.n * p.c.group <= 8 ? rows_launch<T, D, 1>(p, st) : rows_launch<T, D, 2>(p, st);
+}
+
+// Tiles of 8 or 16 query rows.
+cudaError_t cache_rows_launch(RowsParams& p, int d, int dtype, cudaStream_t st) {
   if (dtype == ATTN_JVP_BF16)
     return d == 128 ? rows_launch<__nv_bfloat16, 128>(p, st) : rows_launch<__nv_bfloat16, 64>(p, st);
   return d == 128 ? rows_launch<__half, 128>(p, st) : rows_launch<__half, 64>(p, st);
 }
+
+}  // namespace
 
 }  // namespace ajvp_serve
 
@@ -509,7 +577,8 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
     return ATTN_JVP_ERR_MISALIGNED;
   if ((s.B > 1 && q_strides[0] < 0) || (s.L > 1 && q_strides[1] < 0) || (s.H > 1 && q_strides[2] < 0))
     return ATTN_JVP_ERR_INVALID_ARGUMENT;
-  CacheAttnParams p;
+  RowsParams rp;
+  CacheAttnParams& p = rp.c;
   int sms = 0;
   rc = ajvp::device_status_word(&p.status, &sms);
   if (rc != ATTN_JVP_OK) return rc;
@@ -543,8 +612,18 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
   if (few)
     while (p.splits < 8 && tiles * p.splits < 2 * sms && len >= 256 * p.splits) p.splits *= 2;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = few ? cache_rows_launch(p, static_cast<int>(s.d), s.dtype, st)
-                            : cache_tiles_launch(p, len, static_cast<int>(s.d), s.dtype, st);
+  cudaError_t e;
+  if (few) {
+    rp.box = cache->page_tokens < kStep ? static_cast<int>(cache->page_tokens) : kStep;
+    if (!ajvp::encode_cache_map(&rp.map_k, cache->k, s.d, cache->page_tokens, Hkv, cache->pages,
+                                p.token_stride, p.head_stride, p.page_stride, rp.box) ||
+        !ajvp::encode_cache_map(&rp.map_v, cache->v, s.d, cache->page_tokens, Hkv, cache->pages,
+                                p.token_stride, p.head_stride, p.page_stride, rp.box))
+      return ATTN_JVP_ERR_INVALID_ARGUMENT;
+    e = cache_rows_launch(rp, static_cast<int>(s.d), s.dtype, st);
+  } else {
+    e = cache_tiles_launch(p, len, static_cast<int>(s.d), s.dtype, st);
+  }
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? ATTN_JVP_OK : ATTN_JVP_ERR_CUDA;
 }

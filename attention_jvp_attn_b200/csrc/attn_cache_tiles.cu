@@ -57,14 +57,6 @@ struct TilesCfg {
   static_assert(STATS_AT + 2 * 2 * kTile * 4 <= DATA, "the joined sums lie over the tiles");
 };
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 template <int D, typename T>
 __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __grid_constant__ CacheAttnParams p) {
   using C = TilesCfg<D>;

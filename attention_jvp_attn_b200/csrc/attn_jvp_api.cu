@@ -577,6 +577,25 @@ bool encode_token_rows_map(CUtensorMap* map, const void* base, int32_t dtype, in
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_cache_map(CUtensorMap* map, const void* base, int64_t d, int64_t page_tokens,
+                      int64_t heads, int64_t pages, int64_t token_stride, int64_t head_stride,
+                      int64_t page_stride, int box_rows) {
+  if (!g_encode) return false;
+  if (heads == 1) head_stride = d;  // as above
+  if (pages == 1) page_stride = d;
+  const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(page_tokens), cuuint64_t(heads),
+                              cuuint64_t(pages)};
+  const cuuint64_t strides[3] = {cuuint64_t(token_stride), cuuint64_t(head_stride),
+                                 cuuint64_t(page_stride)};
+  const cuuint32_t box[4] = {cuuint32_t(d), cuuint32_t(box_rows), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace ajvp
 
 extern "C" {

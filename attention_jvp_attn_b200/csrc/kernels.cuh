@@ -116,5 +116,11 @@ bool encode_bf16_rows_map(CUtensorMap* map, const void* base, int64_t B, int64_t
 bool encode_token_rows_map(CUtensorMap* map, const void* base, int32_t dtype, int64_t T,
                            int64_t heads, int64_t d, int64_t token_stride, int64_t head_stride,
                            int box_rows);
+// 4-D tensor map over a page pool of bytes (d, page tokens, heads, pages) with
+// strides in bytes: boxes of d x `box_rows` tokens of one head and page,
+// swizzled by the row's d bytes (128 or 64).
+bool encode_cache_map(CUtensorMap* map, const void* base, int64_t d, int64_t page_tokens,
+                      int64_t heads, int64_t pages, int64_t token_stride, int64_t head_stride,
+                      int64_t page_stride, int box_rows);
 
 }  // namespace ajvp

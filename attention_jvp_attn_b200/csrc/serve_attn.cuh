@@ -75,9 +75,16 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
-// attn_cache_rows.cu: tiles of 16 query rows on warp-level matrix instructions
-cudaError_t cache_rows_launch(const CacheAttnParams& p, int d, int dtype, cudaStream_t st);
-constexpr int kRowsTile = 16;
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+constexpr int kRowsTile = 16;  // most query rows per key head of attn_cache_rows.cu
 // attn_cache_tiles.cu: pairs of tiles of 128 query rows on tcgen05; sets p.splits
 // for sequences of up to `keys` tokens
 cudaError_t cache_tiles_launch(CacheAttnParams& p, int64_t keys, int d, int dtype, cudaStream_t st);
