@@ -154,8 +154,10 @@ def load(path: str = None) -> ctypes.CDLL:
         lib.attn_jvp_cache_append.restype = ctypes.c_int
         lib.attn_jvp_cache_attn.argtypes = [ctypes.POINTER(Shape), i64, vp, ctypes.POINTER(i64),
                                             ctypes.POINTER(Cache), vp, vp, i64, i64, i64, i32, vp,
-                                            vp, vp]
+                                            i64, vp, vp, vp]
         lib.attn_jvp_cache_attn.restype = ctypes.c_int
+        lib.attn_jvp_cache_attn_workspace_bytes.argtypes = [ctypes.POINTER(Shape), i64, i64]
+        lib.attn_jvp_cache_attn_workspace_bytes.restype = i64
         lib.attn_jvp_prompt_attn.argtypes = [ctypes.POINTER(Tokens), vp, Strides, vp, Strides, vp,
                                              Strides, i64, vp, vp, vp, vp]
         lib.attn_jvp_prompt_attn.restype = ctypes.c_int

@@ -25,9 +25,16 @@
 // holds up no other. The order of the head dimension inside the products is
 // free, so a lane takes 16 adjacent codes at a time for four matrix
 // instructions, and the column order of O lets a lane own adjacent columns: no
-// shared-memory transposes. The key axis of one tile is split over the blocks
-// of a cluster, which join their sums through distributed shared memory: one
-// launch, no workspace, a fixed order of sums.
+// shared-memory transposes.
+//
+// The key axis is split in one of two ways, both with a fixed order of sums:
+//   - short sequences: over the blocks of a cluster, which join their sums
+//     through distributed shared memory. One launch, which counts there;
+//   - long ones: all steps of all sequences and heads in a row are shared out
+//     evenly to as many blocks as fit at once, so sequences of any lengths
+//     load the SMs evenly. A block's first and last pieces may be parts of a
+//     sequence; their sums go to the workspace, and a second, small kernel
+//     joins them.
 #include <cuda.h>
 
 #include "serve_attn.cuh"
@@ -45,7 +52,8 @@ constexpr uint32_t kHidden = 0xffffffffu;  // in place of a key scale: no page t
 struct RowsParams {
   CUtensorMap map_k, map_v;  // codes (d, page tokens, heads, pages), boxes of d x box tokens
   CacheAttnParams c;
-  int box;  // 16 or 32 tokens, one page's
+  int box;      // 16 or 32 tokens, one page's
+  float* work;  // sums of partial pieces, two places per block; null: clusters
 };
 
 template <int D, int NT>
@@ -64,7 +72,70 @@ struct RowsCfg {
   static constexpr int AT_BARS = AT_SCALES + kRowsWarps * SCALES;
   static constexpr int BYTES = 1024 + AT_BARS + kRowsWarps * STAGES * 8 + 16;
   static_assert(PART <= SLOT && SLOT % 1024 == 0 && AT_BARS % 8 == 0, "layout");
+  // a place of the workspace: the block's sums, then maxima and sums of p
+  static constexpr int PLACE = ROWS * (D + 2);
 };
+
+// Steps of a sequence of which `reach` tokens are seen; one without tokens
+// takes a step of its own, in which its empty rows are written.
+__device__ __forceinline__ int steps_of(int reach) { return max((reach + kStep - 1) / kStep, 1); }
+
+// Tokens that the last of sequence b's new ones sees (all of them: rows <= 16).
+__device__ __forceinline__ int reach_of(const CacheAttnParams& p, int b) {
+  return checked_len(p, b);
+}
+
+// All steps, Hkv times those of each sequence, and the sequence that holds
+// step `w` with the number of steps before it. The whole block calls this.
+__device__ __forceinline__ void find_step(const CacheAttnParams& p, int64_t share, int64_t blocks,
+                                          int64_t& all, int& b, int64_t& before) {
+  __shared__ int64_t warp_sum[kRowsWarps];
+  __shared__ int64_t at[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kThreads = kRowsWarps * 32;
+  auto own = [&](int i) -> int64_t { return i < p.B ? int64_t(p.Hkv) * steps_of(reach_of(p, i)) : 0; };
+  // inclusive sums of 128 sequences at a time
+  auto scan = [&](int64_t x, int64_t& total) -> int64_t {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    total = 0;
+    int64_t base = 0;
+#pragma unroll
+    for (int w = 0; w < kRowsWarps; ++w) {
+      if (w < warp) base += warp_sum[w];
+      total += warp_sum[w];
+    }
+    return base + x;
+  };
+  all = 0;
+  const int64_t first = own(threadIdx.x);  // kept for the second pass
+  for (int i0 = 0; i0 < p.B; i0 += kThreads) {
+    int64_t total;
+    scan(i0 == 0 ? first : own(i0 + threadIdx.x), total);
+    all += total;
+  }
+  const int64_t w = all * share / blocks;
+  int64_t passed = 0;
+  for (int i0 = 0; i0 < p.B; i0 += kThreads) {
+    const int64_t x = i0 == 0 ? first : own(i0 + threadIdx.x);
+    int64_t total;
+    const int64_t end = passed + scan(x, total);
+    if (w < end && w >= end - x) {
+      at[0] = i0 + threadIdx.x;
+      at[1] = end - x;
+    }
+    passed += total;
+  }
+  __syncthreads();
+  b = static_cast<int>(at[0]);
+  before = at[1];
+}
 
 // A lane's place in the instruction: g = lane / 4 its token (or column of O),
 // c = lane % 4 its columns (or tokens). Which tokens and which 16 codes those
@@ -101,6 +172,27 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) { return Elem<__h
 __device__ __forceinline__ uint32_t lo16(uint32_t w) { return e4m3x2_to_f16x2(w & 0xffffu); }
 __device__ __forceinline__ uint32_t hi16(uint32_t w) { return e4m3x2_to_f16x2(w >> 16); }
 
+// Four columns of row r of (b, hk) from its sums.
+template <typename T, int D>
+__device__ __forceinline__ void write_row(const CacheAttnParams& p, int b, int hk, int r, int col,
+                                          const float4& y, float top, float sum) {
+  const int token = r / p.group, head = hk * p.group + r - token * p.group;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen (a NaN sum is not 0)
+  T* dst = static_cast<T*>(p.o) + ((int64_t(b) * p.n + token) * p.H + head) * D + col;
+  uint2 u;
+  u.x = Elem<T>::pack(y.x * inv, y.y * inv);
+  u.y = Elem<T>::pack(y.z * inv, y.w * inv);
+  *reinterpret_cast<uint2*>(dst) = u;
+  if (col == 0)
+    p.lse[(int64_t(b) * p.H + head) * p.n + token] =
+        sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// Orders this thread's shared-memory accesses before later copies into it.
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __grid_constant__ RowsParams params) {
   using C = RowsCfg<D, NT>;
@@ -116,12 +208,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
   volatile int* abort_flag =
       reinterpret_cast<volatile int*>(smem + C::AT_BARS + kRowsWarps * C::STAGES * 8);
 
-  const int tile = blockIdx.x / p.splits, rank = blockIdx.x - tile * p.splits;
-  const int rt = tile % p.row_tiles, bh = tile / p.row_tiles;
-  const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
-  const int rows = p.n * p.group;  // rows of this key head: token-major, then head of the group
-  const int row0 = rt * C::ROWS;
-  const int len = checked_len(p, b);
+  const int rows = p.n * p.group;  // rows of a key head: token-major, then head of the group
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
     for (int i = 0; i < C::STAGES; ++i) ajvp::mbar_init(&full[i], 1);
@@ -129,401 +216,502 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
   }
   __syncthreads();
 
-  const int last = min(row0 + C::ROWS, rows) - 1;
-  const int reach = p.causal ? max(len - p.n + last / p.group + 1, 0) : len;  // most keys seen
-  const int all = p.causal ? max(len - p.n + row0 / p.group + 1, 0) : len;    // keys all rows see
-  const int steps = (reach + kStep - 1) / kStep;
-  const int s_begin = static_cast<int>(int64_t(steps) * rank / p.splits);
-  const int s_end = static_cast<int>(int64_t(steps) * (rank + 1) / p.splits);
-
+  // This block's pieces: steps [s_begin, s_end) of sequence b and key head hk,
+  // one piece of a cluster's, or the steps [w, w_end) of all in a row.
+  int b, hk, rank = 0;
+  int64_t w = 0, w_end = 1, base = 0;  // base: the first step of (b, hk)
+  if (params.work) {
+    int64_t all;
+    find_step(p, blockIdx.x, gridDim.x, all, b, base);
+    w = all * blockIdx.x / gridDim.x;
+    w_end = all * (blockIdx.x + 1) / gridDim.x;
+    const int steps = steps_of(reach_of(p, b));
+    hk = static_cast<int>((w - base) / steps);
+    base += int64_t(hk) * steps;
+  } else {
+    const int tile = blockIdx.x / p.splits;
+    rank = blockIdx.x - tile * p.splits;
+    b = tile / p.Hkv;
+    hk = tile - b * p.Hkv;
+  }
   uint8_t* ring = smem + warp * C::SLOT;
   float* scales = reinterpret_cast<float*>(smem + C::AT_SCALES + warp * C::SCALES);
-
-  // Pages of step s: lanes 0 and 1 those of its 16-token halves; -1: none.
-  auto page_of = [&](int s) -> int {
-    const int j = s * kStep + (lane & 1) * 16;
-    return lane < 2 && s < s_end && j < reach ? checked_page(p, b, j) : -1;
-  };
-  // Copies step s, whose pages are `page`, into stage st. Returns what lanes
-  // 0 to 3 will put into the stage's scales: keys (0, 1) and values (2, 3) of
-  // the halves, a mark for a hidden half's keys.
   int issued = 0, taken = 0;  // steps whose copies were issued, and waited for
-  auto fetch = [&](int s, int st, int page) -> float {
-    const int page0 = __shfl_sync(0xffffffffu, page, 0), page1 = __shfl_sync(0xffffffffu, page, 1);
-    float sc = lane < 2 ? __uint_as_float(kHidden) : 1.f;
-    if (s < s_end) {
-      ++issued;
-      uint8_t* at = ring + st * 2 * C::KV;
-      const int j = (s * kStep) & ((1 << p.page_shift) - 1);
-      if (lane == 0) {
-        const int boxes = params.box == kStep ? (page0 >= 0) : (page0 >= 0) + (page1 >= 0);
-        ajvp::mbar_arrive_expect_tx(&full[st], boxes * params.box * D * 2);
-        if (page0 >= 0) {
-          ajvp::tma_load_4d(at, &params.map_k, &full[st], 0, j, hk, page0);
-          ajvp::tma_load_4d(at + C::KV, &params.map_v, &full[st], 0, j, hk, page0);
+  bool first_piece = true;
+  while (w < w_end) {
+    const int len = checked_len(p, b);
+    const int reach = len;  // most keys seen
+    const int all = p.causal ? max(len - p.n + 1, 0) : len;  // keys all rows see
+    const int steps = params.work ? steps_of(reach) : (reach + kStep - 1) / kStep;
+    int s_begin, s_end;
+    if (params.work) {
+      s_begin = static_cast<int>(w - base);
+      s_end = static_cast<int>(min(w_end - base, int64_t(steps)));
+    } else {
+      s_begin = static_cast<int>(int64_t(steps) * rank / p.splits);
+      s_end = static_cast<int>(int64_t(steps) * (rank + 1) / p.splits);
+    }
+    const bool whole = s_begin == 0 && s_end == steps;
+
+    // Pages of step s: lanes 0 and 1 those of its 16-token halves; -1: none.
+    auto page_of = [&](int s) -> int {
+      const int j = s * kStep + (lane & 1) * 16;
+      return lane < 2 && s < s_end && j < reach ? checked_page(p, b, j) : -1;
+    };
+    // Copies step s, whose pages are `page`, into the next stage. Returns what
+    // lanes 0 to 3 will put into the stage's scales: keys (0, 1) and values
+    // (2, 3) of the halves, a mark for a hidden half's keys.
+    auto fetch = [&](int s, int page) -> float {
+      const int page0 = __shfl_sync(0xffffffffu, page, 0), page1 = __shfl_sync(0xffffffffu, page, 1);
+      float sc = lane < 2 ? __uint_as_float(kHidden) : 1.f;
+      if (s < s_end) {
+        const int st = issued++ % C::STAGES;
+        uint8_t* at = ring + st * 2 * C::KV;
+        const int j = (s * kStep) & ((1 << p.page_shift) - 1);
+        if (lane == 0) {
+          const int boxes = params.box == kStep ? (page0 >= 0) : (page0 >= 0) + (page1 >= 0);
+          ajvp::mbar_arrive_expect_tx(&full[st], boxes * params.box * D * 2);
+          if (page0 >= 0) {
+            ajvp::tma_load_4d(at, &params.map_k, &full[st], 0, j, hk, page0);
+            ajvp::tma_load_4d(at + C::KV, &params.map_v, &full[st], 0, j, hk, page0);
+          }
+          if (params.box != kStep && page1 >= 0) {
+            ajvp::tma_load_4d(at + 16 * D, &params.map_k, &full[st], 0, 0, hk, page1);
+            ajvp::tma_load_4d(at + C::KV + 16 * D, &params.map_v, &full[st], 0, 0, hk, page1);
+          }
         }
-        if (params.box != kStep && page1 >= 0) {
-          ajvp::tma_load_4d(at + 16 * D, &params.map_k, &full[st], 0, 0, hk, page1);
-          ajvp::tma_load_4d(at + C::KV + 16 * D, &params.map_v, &full[st], 0, 0, hk, page1);
-        }
+        const int pg = (lane & 1) ? page1 : page0;
+        if (lane < 4 && pg >= 0) sc = p.scale[lane >> 1][pg * p.scale_page + hk * p.scale_head];
       }
-      const int pg = (lane & 1) ? page1 : page0;
-      if (lane < 4 && pg >= 0) sc = p.scale[lane >> 1][pg * p.scale_page + hk * p.scale_head];
-    }
-    return sc;
-  };
+      return sc;
+    };
 
-  int next = s_begin + warp;  // next step to copy
-  int page = page_of(next);
-  float pending = 0.f;
+    int next = s_begin + warp;  // next step to copy
+    int page = page_of(next);
+    float pending = 0.f;
 #pragma unroll
-  for (int i = 0; i < C::STAGES - 1; ++i) {
-    pending = fetch(next, i, page);
-    next += kRowsWarps;
-    page = page_of(next);
-    if (lane < 4) scales[4 * i + lane] = pending;
-  }
-
-  // Queries as fp16 fragments: k-step (h, s) holds columns (c + 4h) 16 + 4s + 0..3 of row g.
-  uint32_t q[NT][H2][4][2];
-  float row_scale[NT][2];  // of rows 2c, 2c + 1
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int r = row0 + 8 * t + g;
-    float x[H2][16];
-    float amax = 0.f;
-    const int token = r / p.group, head = hk * p.group + r - token * p.group;
-    const T* src = static_cast<const T*>(p.q) + b * p.q_seq + token * p.q_token + head * p.q_head;
-#pragma unroll
-    for (int h = 0; h < H2; ++h) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float (&y)[8] = reinterpret_cast<float(&)[8]>(x[h][8 * j]);
-        if (r < rows) {
-          load8(src + (c + 4 * h) * 16 + 8 * j, y);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float a = fabsf(y[e]);
-          amax = fmaxf(amax, a < INFINITY ? a : 0.f);
-        }
-      }
-    }
-    float inv = 1.f, mine = p.scale_log2;
-    if constexpr (!std::is_same<T, __half>::value) {
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      int e = 0;
-      if (amax > 0.f) frexpf(amax, &e);
-      e = min(max(e, -100), 100);
-      inv = ldexpf(1.f, -e);
-      mine *= ldexpf(1.f, e);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) row_scale[t][i] = __shfl_sync(0xffffffffu, mine, 4 * (2 * c + i));
-#pragma unroll
-    for (int h = 0; h < H2; ++h)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        q[t][h][s][0] = pack_f16(x[h][4 * s] * inv, x[h][4 * s + 1] * inv);
-        q[t][h][s][1] = pack_f16(x[h][4 * s + 2] * inv, x[h][4 * s + 3] * inv);
-      }
-  }
-  int seen[NT][2];  // keys that rows 2c, 2c + 1 see
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = min(row0 + 8 * t + 2 * c + i, rows - 1);
-      seen[t][i] = p.causal ? max(len - p.n + r / p.group + 1, 0) : len;
+    for (int i = 0; i < C::STAGES - 1; ++i) {
+      const int st = issued % C::STAGES;
+      pending = fetch(next, page);
+      next += kRowsWarps;
+      page = page_of(next);
+      if (lane < 4) scales[4 * st + lane] = pending;
     }
 
-  float m[NT][2], l[NT][2], acc[NT][VB / 2][4];
+    // Queries as fp16 fragments: k-step (h, s) holds columns (c + 4h) 16 + 4s + 0..3 of row g.
+    uint32_t q[NT][H2][4][2];
+    float row_scale[NT][2];  // of rows 2c, 2c + 1
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) m[t][i] = -INFINITY, l[t][i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < VB / 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][j][i] = 0.f;
-  }
-
-  int stage = 0, into = C::STAGES - 1;
-  uint32_t phase = 0;
-  bool late = false;  // `pending` belongs to the stage before `into`
-  __syncwarp();
-  for (int s = s_begin + warp; s < s_end; s += kRowsWarps) {
-    if (late && lane < 4) scales[4 * (into == 0 ? C::STAGES - 1 : into - 1) + lane] = pending;
-    // the stage's reads are over since the end of the last round
-    pending = fetch(next, into, page);
-    late = true;
-    next += kRowsWarps;
-    page = page_of(next);
-    if (++into == C::STAGES) into = 0;
-    if (!ajvp::warp_wait(&full[stage], phase, abort_flag, p.status)) break;
-    ++taken;
-    __syncwarp();
-    const uint8_t* sk = ring + stage * 2 * C::KV;
-    const uint8_t* sv = sk + C::KV;
-    const float4 ss = *reinterpret_cast<const float4*>(scales + 4 * stage);
-
-    float x[NT][2][4];  // 16-token halves: token g (0, 1) and g + 8 (2, 3), rows 2c (0, 2), 2c + 1
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) x[t][f][0] = x[t][f][1] = x[t][f][2] = x[t][f][3] = 0.f;
-      const int r = 16 * f + token_of<D>(g);
+    for (int t = 0; t < NT; ++t) {
+      const int r = 8 * t + g;
+      float x[H2][16];
+      float amax = 0.f;
+      const int token = r / p.group, head = hk * p.group + r - token * p.group;
+      const T* src = static_cast<const T*>(p.q) + b * p.q_seq + token * p.q_token + head * p.q_head;
 #pragma unroll
       for (int h = 0; h < H2; ++h) {
-        const uint4 u = *reinterpret_cast<const uint4*>(sk + place<D>(r, c + 4 * h));
-        const uint4 w = *reinterpret_cast<const uint4*>(sk + place<D>(r + 8, c + 4 * h));
-        const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t a0 = lo16(us[e]), a1 = lo16(ws[e]), a2 = hi16(us[e]), a3 = hi16(ws[e]);
+        for (int j = 0; j < 2; ++j) {
+          float (&y)[8] = reinterpret_cast<float(&)[8]>(x[h][8 * j]);
+          if (r < rows) {
+            load8(src + (c + 4 * h) * 16 + 8 * j, y);
+          } else {
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(x[t][f], a0, a1, a2, a3, q[t][h][e][0], q[t][h][e][1]);
-        }
-      }
-    }
-    // scores in powers of two, the value scale in the exponent
-    const bool hidden[2] = {__float_as_uint(ss.x) == kHidden, __float_as_uint(ss.y) == kHidden};
-    const float ks[2] = {read_scale(ss.x), read_scale(ss.y)};
-    const float vs[2] = {read_scale(ss.z), read_scale(ss.w)};
-    const float lv[2] = {log2_approx(vs[0]), log2_approx(vs[1])};
-    const int j0 = s * kStep;
-    const bool edge = j0 + kStep > all || hidden[0] || hidden[1];
-    float top[NT][2];
+            for (int e = 0; e < 8; ++e) y[e] = 0.f;
+          }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[t][f][e] = fmaf(x[t][f][e], row_scale[t][e & 1] * ks[f], lv[f]);
-      if (edge) {
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (hidden[f] || j0 + 16 * f + token_of<D>(g) + 8 * (e >> 1) >= seen[t][e & 1])
-              x[t][f][e] = -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        top[t][i] = fmaxf(fmaxf(x[t][0][i], x[t][0][i + 2]), fmaxf(x[t][1][i], x[t][1][i + 2]));
-    }
-    bool raise = false;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) raise |= top[t][i] > m[t][i] + kLazyMax;
-    if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float to = top[t][i];
-          to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 4));
-          to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 8));
-          to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 16));
-          to = fmaxf(to, m[t][i]);
-          const float f = to == -INFINITY ? 1.f : ajvp::ex2_approx(m[t][i] - to);
-          m[t][i] = to;
-          l[t][i] *= f;
-#pragma unroll
-          for (int j = 0; j < VB / 2; ++j) {
-            acc[t][j][i] *= f;
-            acc[t][j][2 + i] *= f;
+          for (int e = 0; e < 8; ++e) {
+            const float a = fabsf(y[e]);
+            amax = fmaxf(amax, a < INFINITY ? a : 0.f);
           }
         }
-    }
-    uint32_t pk[NT][2][2], vis[NT][2][2];  // probabilities, and 1.0 where a row sees a token
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float base[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const float inv_v = 1.f / vs[f];
-        if (edge) {
-          vis[t][f][0] = transpose8(pack_f16(x[t][f][0] != -INFINITY, x[t][f][1] != -INFINITY));
-          vis[t][f][1] = transpose8(pack_f16(x[t][f][2] != -INFINITY, x[t][f][3] != -INFINITY));
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[t][f][e] = ajvp::ex2_approx(x[t][f][e] - base[e & 1]);
-        l[t][0] = fmaf(x[t][f][0] + x[t][f][2], inv_v, l[t][0]);
-        l[t][1] = fmaf(x[t][f][1] + x[t][f][3], inv_v, l[t][1]);
-        pk[t][f][0] = transpose8(pack_f16(x[t][f][0], x[t][f][1]));
-        pk[t][f][1] = transpose8(pack_f16(x[t][f][2], x[t][f][3]));
       }
-    }
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      // values of the instruction's tokens 2c, 2c + 1, 2c + 8, 2c + 9, the lane's columns
-      uint32_t w[4][VB / 4];
-      bool nan = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 16 * f + token_of<D>(2 * c + (i & 1)) + 8 * (i >> 1);
-        if constexpr (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sv + place<D>(r, token_of<D>(g)));
-          w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(sv + place<D>(r, g >> 1) + 8 * (g & 1));
-          w[i][0] = u.x, w[i][1] = u.y;
-        }
-        if (edge) {
-#pragma unroll
-          for (int e = 0; e < VB / 4; ++e)
-            nan |= (((w[i][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
-        }
+      float inv = 1.f, mine = p.scale_log2;
+      if constexpr (!std::is_same<T, __half>::value) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        int e = 0;
+        if (amax > 0.f) frexpf(amax, &e);
+        e = min(max(e, -100), 100);
+        inv = ldexpf(1.f, -e);
+        mine *= ldexpf(1.f, e);
       }
-      // A NaN value where some rows see the token and some do not (or none: what
-      // an earlier owner of the page left there): it must not reach the rows
-      // that do not (0 * NaN). It is taken out of the product, and a second
-      // product, of what each row sees and where the NaN are, says which sums
-      // become NaN.
-      const bool apart = edge && __any_sync(0xffffffffu, nan);
 #pragma unroll
-      for (int e = 0; e < VB / 4; ++e)
+      for (int i = 0; i < 2; ++i) row_scale[t][i] = __shfl_sync(0xffffffffu, mine, 4 * (2 * c + i));
 #pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-          // bytes 2hi, 2hi + 1 of the two tokens of a pair, interleaved
-          const uint32_t sel = hi ? 0x7362u : 0x5140u;
-          uint32_t p0 = __byte_perm(w[0][e], w[1][e], sel), p1 = __byte_perm(w[2][e], w[3][e], sel);
-          const int j = 2 * e + hi;
-          if (apart) {
-            const uint32_t n0 = (((p0 & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
-            const uint32_t n1 = (((p1 & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
-            p0 &= ~(n0 * 0xffu);
-            p1 &= ~(n1 * 0xffu);
+      for (int h = 0; h < H2; ++h)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              float hit[4] = {0.f, 0.f, 0.f, 0.f};
-              // 0x38 is the e4m3 code of 1
-              mma_f16(hit, lo16(n0 * 0x38u), hi16(n0 * 0x38u), lo16(n1 * 0x38u), hi16(n1 * 0x38u),
-                      vis[t][f][0], vis[t][f][1]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (hit[i] > 0.f) acc[t][j][i] = NAN;
-            }
-          }
-          const uint32_t a0 = lo16(p0), a1 = hi16(p0), a2 = lo16(p1), a3 = hi16(p1);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(acc[t][j], a0, a1, a2, a3, pk[t][f][0], pk[t][f][1]);
+        for (int s = 0; s < 4; ++s) {
+          q[t][h][s][0] = pack_f16(x[h][4 * s] * inv, x[h][4 * s + 1] * inv);
+          q[t][h][s][1] = pack_f16(x[h][4 * s + 2] * inv, x[h][4 * s + 3] * inv);
         }
     }
-    __syncwarp();
-    if (++stage == C::STAGES) stage = 0, phase ^= 1;
-  }
-  // After an abort copies may still be on their way: they land before the ring
-  // is written over. (A normal end has waited for each.)
-  for (; taken < issued; ++taken)
-    ajvp::mbar_wait_drain(&full[taken % C::STAGES], (taken / C::STAGES) & 1, 200000000ull);
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 4);
-      l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 8);
-      l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 16);
-    }
-
-  // Join the warps: each leaves its sums in its ring, then the block adds them
-  // up into `whole`, and the cluster's blocks add those up.
-  float* whole = reinterpret_cast<float*>(smem + C::AT_WHOLE);
-  float* wm = reinterpret_cast<float*>(smem + C::AT_STATS);  // [warps][ROWS]: running maxima
-  float* wl = wm + C::ROWS * kRowsWarps;                     // [warps][ROWS]: sums
-  float* bm = wl + C::ROWS * kRowsWarps;                     // [ROWS]: the block's maxima, then sums
-  __syncwarp();
-  {
-    float* part = reinterpret_cast<float*>(ring);
-    const int col = D == 128 ? token_of<D>(g) * VB : g * VB;
+    int seen[NT][2];  // keys that rows 2c, 2c + 1 see
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = 8 * t + 2 * c + i;
+        const int r = min(8 * t + 2 * c + i, rows - 1);
+        seen[t][i] = p.causal ? max(len - p.n + r / p.group + 1, 0) : len;
+      }
+
+    float m[NT][2], l[NT][2], acc[NT][VB / 2][4];
 #pragma unroll
-        for (int j = 0; j < VB / 2; j += 2)
-          *reinterpret_cast<float4*>(part + r * C::PITCH + col + 2 * j) =
-              make_float4(acc[t][j][i], acc[t][j][2 + i], acc[t][j + 1][i], acc[t][j + 1][2 + i]);
-        if (g == 0) {
-          wm[warp * C::ROWS + r] = m[t][i];
-          wl[warp * C::ROWS + r] = l[t][i];
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m[t][i] = -INFINITY, l[t][i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < VB / 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][j][i] = 0.f;
+    }
+
+    int late = -1;  // the stage that `pending` belongs to
+    __syncwarp();
+    for (int s = s_begin + warp; s < s_end; s += kRowsWarps) {
+      if (late >= 0 && lane < 4) scales[4 * late + lane] = pending;
+      // the next stage's reads are over since the end of the last round
+      late = next < s_end ? issued % C::STAGES : -1;
+      pending = fetch(next, page);
+      next += kRowsWarps;
+      page = page_of(next);
+      const int stage = taken % C::STAGES;
+      if (!ajvp::warp_wait(&full[stage], (taken / C::STAGES) & 1, abort_flag, p.status)) break;
+      ++taken;
+      __syncwarp();
+      const uint8_t* sk = ring + stage * 2 * C::KV;
+      const uint8_t* sv = sk + C::KV;
+      const float4 ss = *reinterpret_cast<const float4*>(scales + 4 * stage);
+
+      float x[NT][2][4];  // 16-token halves: token g (0, 1) and g + 8 (2, 3), rows 2c (0, 2), 2c + 1
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) x[t][f][0] = x[t][f][1] = x[t][f][2] = x[t][f][3] = 0.f;
+        const int r = 16 * f + token_of<D>(g);
+#pragma unroll
+        for (int h = 0; h < H2; ++h) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sk + place<D>(r, c + 4 * h));
+          const uint4 w = *reinterpret_cast<const uint4*>(sk + place<D>(r + 8, c + 4 * h));
+          const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a0 = lo16(us[e]), a1 = lo16(ws[e]), a2 = hi16(us[e]), a3 = hi16(ws[e]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma_f16(x[t][f], a0, a1, a2, a3, q[t][h][e][0], q[t][h][e][1]);
+          }
         }
       }
-  }
-  __syncthreads();
-  constexpr int kThreads = kRowsWarps * 32;
-  for (int item = threadIdx.x; item < C::ROWS * (D / 4); item += kThreads) {
-    const int r = item / (D / 4), col = (item % (D / 4)) * 4;
-    float top = -INFINITY;
+      // scores in powers of two, the value scale in the exponent
+      const bool hidden[2] = {__float_as_uint(ss.x) == kHidden, __float_as_uint(ss.y) == kHidden};
+      const float ks[2] = {read_scale(ss.x), read_scale(ss.y)};
+      const float vs[2] = {read_scale(ss.z), read_scale(ss.w)};
+      const float lv[2] = {log2_approx(vs[0]), log2_approx(vs[1])};
+      const int j0 = s * kStep;
+      const bool edge = j0 + kStep > all || hidden[0] || hidden[1];
+      float top[NT][2];
 #pragma unroll
-    for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, wm[w * C::ROWS + r]);
-    float sum = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int w = 0; w < kRowsWarps; ++w) {
-      // a warp that saw no key has sum 0 and maximum -inf; NaN sums pass on
-      const float f = top == -INFINITY ? 1.f : ajvp::ex2_approx(wm[w * C::ROWS + r] - top);
-      sum = fmaf(wl[w * C::ROWS + r], f, sum);
-      const float4 z = *reinterpret_cast<const float4*>(smem + w * C::SLOT + (r * C::PITCH + col) * 4);
-      y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y);
-      y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[t][f][e] = fmaf(x[t][f][e], row_scale[t][e & 1] * ks[f], lv[f]);
+        if (edge) {
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (hidden[f] || j0 + 16 * f + token_of<D>(g) + 8 * (e >> 1) >= seen[t][e & 1])
+                x[t][f][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          top[t][i] = fmaxf(fmaxf(x[t][0][i], x[t][0][i + 2]), fmaxf(x[t][1][i], x[t][1][i + 2]));
+      }
+      bool raise = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) raise |= top[t][i] > m[t][i] + kLazyMax;
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float to = top[t][i];
+            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 4));
+            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 8));
+            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 16));
+            to = fmaxf(to, m[t][i]);
+            const float f = to == -INFINITY ? 1.f : ajvp::ex2_approx(m[t][i] - to);
+            m[t][i] = to;
+            l[t][i] *= f;
+#pragma unroll
+            for (int j = 0; j < VB / 2; ++j) {
+              acc[t][j][i] *= f;
+              acc[t][j][2 + i] *= f;
+            }
+          }
+      }
+      uint32_t pk[NT][2][2], vis[NT][2][2];  // probabilities, and 1.0 where a row sees a token
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float base[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const float inv_v = 1.f / vs[f];
+          if (edge) {
+            vis[t][f][0] = transpose8(pack_f16(x[t][f][0] != -INFINITY, x[t][f][1] != -INFINITY));
+            vis[t][f][1] = transpose8(pack_f16(x[t][f][2] != -INFINITY, x[t][f][3] != -INFINITY));
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[t][f][e] = ajvp::ex2_approx(x[t][f][e] - base[e & 1]);
+          l[t][0] = fmaf(x[t][f][0] + x[t][f][2], inv_v, l[t][0]);
+          l[t][1] = fmaf(x[t][f][1] + x[t][f][3], inv_v, l[t][1]);
+          pk[t][f][0] = transpose8(pack_f16(x[t][f][0], x[t][f][1]));
+          pk[t][f][1] = transpose8(pack_f16(x[t][f][2], x[t][f][3]));
+        }
+      }
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        // values of the instruction's tokens 2c, 2c + 1, 2c + 8, 2c + 9, the lane's columns
+        uint32_t w[4][VB / 4];
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * f + token_of<D>(2 * c + (i & 1)) + 8 * (i >> 1);
+          if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(sv + place<D>(r, token_of<D>(g)));
+            w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(sv + place<D>(r, g >> 1) + 8 * (g & 1));
+            w[i][0] = u.x, w[i][1] = u.y;
+          }
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < VB / 4; ++e)
+              nan |= (((w[i][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+          }
+        }
+        // A NaN value where some rows see the token and some do not (or none: what
+        // an earlier owner of the page left there): it must not reach the rows
+        // that do not (0 * NaN). It is taken out of the product, and a second
+        // product, of what each row sees and where the NaN are, says which sums
+        // become NaN.
+        const bool apart = edge && __any_sync(0xffffffffu, nan);
+#pragma unroll
+        for (int e = 0; e < VB / 4; ++e)
+#pragma unroll
+          for (int hi = 0; hi < 2; ++hi) {
+            // bytes 2hi, 2hi + 1 of the two tokens of a pair, interleaved
+            const uint32_t sel = hi ? 0x7362u : 0x5140u;
+            uint32_t p0 = __byte_perm(w[0][e], w[1][e], sel), p1 = __byte_perm(w[2][e], w[3][e], sel);
+            const int j = 2 * e + hi;
+            if (apart) {
+              const uint32_t n0 = (((p0 & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
+              const uint32_t n1 = (((p1 & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
+              p0 &= ~(n0 * 0xffu);
+              p1 &= ~(n1 * 0xffu);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                // 0x38 is the e4m3 code of 1
+                mma_f16(hit, lo16(n0 * 0x38u), hi16(n0 * 0x38u), lo16(n1 * 0x38u), hi16(n1 * 0x38u),
+                        vis[t][f][0], vis[t][f][1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (hit[i] > 0.f) acc[t][j][i] = NAN;
+              }
+            }
+            const uint32_t a0 = lo16(p0), a1 = hi16(p0), a2 = lo16(p1), a3 = hi16(p1);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma_f16(acc[t][j], a0, a1, a2, a3, pk[t][f][0], pk[t][f][1]);
+          }
+      }
+      __syncwarp();
     }
-    *reinterpret_cast<float4*>(whole + r * C::PITCH + col) = y;
-    if (col == 0) bm[r] = top, bm[C::ROWS + r] = sum;
-  }
-  if (p.splits > 1)
-    ajvp::cluster_sync_all();
-  else
-    __syncthreads();
+    // After an abort copies may still be on their way: they land before the ring
+    // is written over. (A normal end has waited for each.)
+    for (; taken < issued; ++taken)
+      ajvp::mbar_wait_drain(&full[taken % C::STAGES], (taken / C::STAGES) & 1, 200000000ull);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 4);
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 8);
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 16);
+      }
 
-  // Block `rank` of the cluster joins and writes every splits-th group of 4 columns.
-  const uint32_t whole_addr = ajvp::smem_u32(whole), bm_addr = ajvp::smem_u32(bm);
-  for (int item = rank + threadIdx.x * p.splits; item < C::ROWS * (D / 4); item += kThreads * p.splits) {
+    // Join the warps: each leaves its sums in its ring, then the block adds them
+    // up into `whole`, and the cluster's blocks add those up.
+    float* sums = reinterpret_cast<float*>(smem + C::AT_WHOLE);
+    float* wm = reinterpret_cast<float*>(smem + C::AT_STATS);  // [warps][ROWS]: running maxima
+    float* wl = wm + C::ROWS * kRowsWarps;                     // [warps][ROWS]: sums
+    float* bm = wl + C::ROWS * kRowsWarps;                     // [ROWS]: the block's maxima, then sums
+    __syncwarp();
+    {
+      float* part = reinterpret_cast<float*>(ring);
+      const int col = D == 128 ? token_of<D>(g) * VB : g * VB;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 8 * t + 2 * c + i;
+#pragma unroll
+          for (int j = 0; j < VB / 2; j += 2)
+            *reinterpret_cast<float4*>(part + r * C::PITCH + col + 2 * j) =
+                make_float4(acc[t][j][i], acc[t][j][2 + i], acc[t][j + 1][i], acc[t][j + 1][2 + i]);
+          if (g == 0) {
+            wm[warp * C::ROWS + r] = m[t][i];
+            wl[warp * C::ROWS + r] = l[t][i];
+          }
+        }
+    }
+    __syncthreads();
+    constexpr int kThreads = kRowsWarps * 32;
+    // what the block's warps have of 4 columns of row r
+    auto block_sums = [&](int r, int col, float& top, float& sum) -> float4 {
+      top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, wm[w * C::ROWS + r]);
+      sum = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kRowsWarps; ++w) {
+        // a warp that saw no key has sum 0 and maximum -inf; NaN sums pass on
+        const float f = top == -INFINITY ? 1.f : ajvp::ex2_approx(wm[w * C::ROWS + r] - top);
+        sum = fmaf(wl[w * C::ROWS + r], f, sum);
+        const float4 z = *reinterpret_cast<const float4*>(smem + w * C::SLOT + (r * C::PITCH + col) * 4);
+        y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y);
+        y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
+      }
+      return y;
+    };
+    if (params.work || p.splits == 1) {
+      float* place = params.work + (2 * int64_t(blockIdx.x) + (first_piece ? 0 : 1)) * C::PLACE;
+      for (int item = threadIdx.x; item < C::ROWS * (D / 4); item += kThreads) {
+        const int r = item / (D / 4), col = (item % (D / 4)) * 4;
+        if (r >= rows) continue;
+        float top, sum;
+        const float4 y = block_sums(r, col, top, sum);
+        if (whole) {
+          write_row<T, D>(p, b, hk, r, col, y, top, sum);
+        } else {
+          *reinterpret_cast<float4*>(place + r * D + col) = y;
+          if (col == 0) place[C::ROWS * D + r] = top, place[C::ROWS * (D + 1) + r] = sum;
+        }
+      }
+      // on to the next piece, whose copies go where these sums are
+      first_piece = false;
+      w = base + s_end;
+      if (!params.work || w >= w_end) break;
+      base = w;
+      if (++hk == p.Hkv) hk = 0, ++b;
+      fence_async();
+      __syncthreads();
+      continue;
+    }
+    // one of a cluster's blocks
+    for (int item = threadIdx.x; item < C::ROWS * (D / 4); item += kThreads) {
+      const int r = item / (D / 4), col = (item % (D / 4)) * 4;
+      float top, sum;
+      *reinterpret_cast<float4*>(sums + r * C::PITCH + col) = block_sums(r, col, top, sum);
+      if (col == 0) bm[r] = top, bm[C::ROWS + r] = sum;
+    }
+    ajvp::cluster_sync_all();
+    // Block `rank` of the cluster joins and writes every splits-th group of 4 columns.
+    const uint32_t sums_addr = ajvp::smem_u32(sums), bm_addr = ajvp::smem_u32(bm);
+    for (int item = rank + threadIdx.x * p.splits; item < C::ROWS * (D / 4); item += kThreads * p.splits) {
+      const int r = item / (D / 4), col = (item % (D / 4)) * 4;
+      if (r >= rows) continue;
+      float top = -INFINITY, sum = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < p.splits; ++k)
+        top = fmaxf(top, ld_cluster_f32(ajvp::mapa_shared(bm_addr + r * 4, k)));
+      for (int k = 0; k < p.splits; ++k) {
+        const float mk = ld_cluster_f32(ajvp::mapa_shared(bm_addr + r * 4, k));
+        const float f = top == -INFINITY ? 1.f : ajvp::ex2_approx(mk - top);
+        sum = fmaf(ld_cluster_f32(ajvp::mapa_shared(bm_addr + (C::ROWS + r) * 4, k)), f, sum);
+        const float4 z = ld_cluster_f32x4(ajvp::mapa_shared(sums_addr + (r * C::PITCH + col) * 4, k));
+        y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y);
+        y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
+      }
+      write_row<T, D>(p, b, hk, r, col, y, top, sum);
+    }
+    ajvp::cluster_sync_all();  // no block leaves while its sums are read
+    break;
+  }
+}
+
+// Joins the pieces of each (sequence, key head) that was shared out over
+// several blocks; a block per (sequence, key head).
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kRowsWarps * 32) join_rows_kernel(const CacheAttnParams p,
+                                                                    const float* work, const int blocks) {
+  using C = RowsCfg<D, NT>;
+  cudaGridDependencySynchronize();  // launched early: the pieces are complete from here on
+  const int b = blockIdx.x / p.Hkv, hk = blockIdx.x - b * p.Hkv;
+  // its steps [g0, g1) of all
+  __shared__ int64_t sums[2][kRowsWarps];
+  int64_t before = 0, all = 0;
+  for (int i = threadIdx.x; i < p.B; i += kRowsWarps * 32) {
+    const int64_t x = int64_t(p.Hkv) * steps_of(reach_of(p, i));
+    all += x;
+    if (i < b) before += x;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if ((threadIdx.x & 31) == 0) sums[0][threadIdx.x >> 5] = all, sums[1][threadIdx.x >> 5] = before;
+  __syncthreads();
+  all = before = 0;
+#pragma unroll
+  for (int w = 0; w < kRowsWarps; ++w) all += sums[0][w], before += sums[1][w];
+  const int steps = steps_of(reach_of(p, b));
+  const int64_t g0 = before + int64_t(hk) * steps, g1 = g0 + steps;
+  // the blocks whose steps, [all k / blocks, all (k + 1) / blocks), meet them
+  int64_t k0 = g0 * blocks / all, k1 = (g1 - 1) * blocks / all;
+  while (k0 > 0 && all * k0 / blocks > g0) --k0;
+  while (all * (k0 + 1) / blocks <= g0) ++k0;
+  while (k1 > 0 && all * k1 / blocks > g1 - 1) --k1;
+  while (all * (k1 + 1) / blocks <= g1 - 1) ++k1;
+  if (k0 == k1) return;  // one block had them all
+  const int rows = p.n * p.group;
+  for (int item = threadIdx.x; item < rows * (D / 4); item += kRowsWarps * 32) {
     const int r = item / (D / 4), col = (item % (D / 4)) * 4;
-    const int row = row0 + r;
-    if (row >= rows) continue;
+    // a block's first piece is in its first place
+    auto place = [&](int64_t k) { return work + (2 * k + (all * k / blocks >= g0 ? 0 : 1)) * C::PLACE; };
     float top = -INFINITY, sum = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < p.splits; ++k)
-      top = fmaxf(top, ld_cluster_f32(ajvp::mapa_shared(bm_addr + r * 4, k)));
-    for (int k = 0; k < p.splits; ++k) {
-      const float mk = ld_cluster_f32(ajvp::mapa_shared(bm_addr + r * 4, k));
-      const float f = top == -INFINITY ? 1.f : ajvp::ex2_approx(mk - top);
-      sum = fmaf(ld_cluster_f32(ajvp::mapa_shared(bm_addr + (C::ROWS + r) * 4, k)), f, sum);
-      const float4 z = ld_cluster_f32x4(ajvp::mapa_shared(whole_addr + (r * C::PITCH + col) * 4, k));
+    for (int64_t k = k0; k <= k1; ++k) {
+      if (all * (k + 1) / blocks <= all * k / blocks) continue;  // a block without steps
+      top = fmaxf(top, place(k)[C::ROWS * D + r]);
+    }
+    for (int64_t k = k0; k <= k1; ++k) {
+      if (all * (k + 1) / blocks <= all * k / blocks) continue;
+      const float* at = place(k);
+      const float f = top == -INFINITY ? 1.f : ajvp::ex2_approx(at[C::ROWS * D + r] - top);
+      const float4 z = *reinterpret_cast<const float4*>(at + r * D + col);
+      sum = fmaf(at[C::ROWS * (D + 1) + r], f, sum);
       y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y);
       y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
     }
-    const int token = row / p.group, head = hk * p.group + row - token * p.group;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen (a NaN sum is not 0)
-    T* dst = static_cast<T*>(p.o) + ((int64_t(b) * p.n + token) * p.H + head) * D + col;
-    uint2 u;
-    u.x = Elem<T>::pack(y.x * inv, y.y * inv);
-    u.y = Elem<T>::pack(y.z * inv, y.w * inv);
-    *reinterpret_cast<uint2*>(dst) = u;
-    if (col == 0)
-      p.lse[(int64_t(b) * p.H + head) * p.n + token] =
-          sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    write_row<T, D>(p, b, hk, r, col, y, top, sum);
   }
-  if (p.splits > 1) ajvp::cluster_sync_all();  // no block leaves while its sums are read
 }
 
 template <typename T, int D, int NT>
-cudaError_t rows_launch(const RowsParams& p, cudaStream_t st) {
+cudaError_t rows_launch(const RowsParams& p, int blocks, cudaStream_t st) {
   using C = RowsCfg<D, NT>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(cache_rows_kernel<T, D, NT>, C::BYTES, done);
+  cudaError_t e = allow_smem(cache_rows_kernel<T, D, NT>, C::BYTES, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.c.B * p.c.Hkv * p.c.row_tiles * p.c.splits));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.work ? blocks : p.c.B * p.c.Hkv * p.c.splits));
   cfg.blockDim = dim3(kRowsWarps * 32);
   cfg.dynamicSmemBytes = C::BYTES;
   cfg.stream = st;
@@ -533,30 +721,61 @@ cudaError_t rows_launch(const RowsParams& p, cudaStream_t st) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_rows_kernel<T, D, NT>, p);
+  e = cudaLaunchKernelEx(&cfg, cache_rows_kernel<T, D, NT>, p);
+  if (e != cudaSuccess || !p.work) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.c.B * p.c.Hkv));
+  cfg.dynamicSmemBytes = 0;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, join_rows_kernel<T, D, NT>, p.c, static_cast<const float*>(p.work),
+                            blocks);
 }
 
 template <typename T, int D>
-cudaError_t rows_launch(const RowsParams& p, cudaStream_t st) {
-  return p.c.n * p.c.group <= 8 ? rows_launch<T, D, 1>(p, st) : rows_launch<T, D, 2>(p, st);
+cudaError_t rows_launch(const RowsParams& p, int blocks, cudaStream_t st) {
+  return p.c.n * p.c.group <= 8 ? rows_launch<T, D, 1>(p, blocks, st)
+                                : rows_launch<T, D, 2>(p, blocks, st);
 }
 
 // Tiles of 8 or 16 query rows.
-cudaError_t cache_rows_launch(RowsParams& p, int d, int dtype, cudaStream_t st) {
+cudaError_t cache_rows_launch(const RowsParams& p, int d, int dtype, int blocks, cudaStream_t st) {
   if (dtype == ATTN_JVP_BF16)
-    return d == 128 ? rows_launch<__nv_bfloat16, 128>(p, st) : rows_launch<__nv_bfloat16, 64>(p, st);
-  return d == 128 ? rows_launch<__half, 128>(p, st) : rows_launch<__half, 64>(p, st);
+    return d == 128 ? rows_launch<__nv_bfloat16, 128>(p, blocks, st)
+                    : rows_launch<__nv_bfloat16, 64>(p, blocks, st);
+  return d == 128 ? rows_launch<__half, 128>(p, blocks, st) : rows_launch<__half, 64>(p, blocks, st);
 }
+
+// Blocks that share out the steps of long sequences: two per SM fit.
+constexpr int kBlocksPerSm = 2;
+
+// Whether sequences of up to `len` tokens are shared out over all blocks (a
+// second launch) rather than split within clusters.
+bool shared_out(int64_t rows, int64_t len) { return rows <= kRowsTile && len > 4096; }
+
+int64_t place_bytes(int64_t rows, int64_t d) { return (rows <= 8 ? 8 : 16) * (d + 2) * 4; }
 
 }  // namespace
 
 }  // namespace ajvp_serve
 
+extern "C" int64_t attn_jvp_cache_attn_workspace_bytes(const attn_jvp_shape* shape, int64_t Hkv,
+                                                       int64_t max_len) {
+  using namespace ajvp_serve;
+  if (!shape || Hkv < 1 || shape->H < 1 || shape->L < 0 || max_len < 0) return -1;
+  const int64_t rows = shape->L * (shape->H / Hkv);
+  if (!shared_out(rows, max_len)) return 0;
+  unsigned int* status = nullptr;
+  int sms = 0;
+  if (ajvp::device_status_word(&status, &sms) != ATTN_JVP_OK) return -1;
+  return 2 * kBlocksPerSm * int64_t(sms) * place_bytes(rows, shape->d);
+}
+
 extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, const void* q,
                                    const int64_t* q_strides, const attn_jvp_cache* cache,
                                    const int32_t* lens, const int32_t* table, int64_t table_width,
-                                   int64_t table_stride, int64_t max_len, int32_t causal, void* o,
-                                   float* lse, void* stream) {
+                                   int64_t table_stride, int64_t max_len, int32_t causal,
+                                   void* workspace, int64_t workspace_bytes, void* o, float* lse,
+                                   void* stream) {
   using namespace ajvp_serve;
   if (!shape || !q_strides) return ATTN_JVP_ERR_INVALID_ARGUMENT;
   const attn_jvp_shape& s = *shape;
@@ -609,7 +828,15 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
   if (rows > (int64_t(1) << 30) || tiles > (int64_t(1) << 27)) return ATTN_JVP_ERR_UNSUPPORTED;
   p.row_tiles = static_cast<int>(row_tiles);
   p.splits = 1;
-  if (few)
+  const bool share = shared_out(rows, len);
+  const int blocks = kBlocksPerSm * sms;
+  if (share) {
+    if (!workspace || workspace_bytes < 2 * blocks * place_bytes(rows, s.d))
+      return ATTN_JVP_ERR_INVALID_ARGUMENT;
+    if (!aligned16(workspace)) return ATTN_JVP_ERR_MISALIGNED;
+  }
+  rp.work = share ? static_cast<float*>(workspace) : nullptr;
+  if (few && !share)
     while (p.splits < 8 && tiles * p.splits < 2 * sms && len >= 256 * p.splits) p.splits *= 2;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -620,7 +847,7 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
         !ajvp::encode_cache_map(&rp.map_v, cache->v, s.d, cache->page_tokens, Hkv, cache->pages,
                                 p.token_stride, p.head_stride, p.page_stride, rp.box))
       return ATTN_JVP_ERR_INVALID_ARGUMENT;
-    e = cache_rows_launch(rp, static_cast<int>(s.d), s.dtype, st);
+    e = cache_rows_launch(rp, static_cast<int>(s.d), s.dtype, blocks, st);
   } else {
     e = cache_tiles_launch(p, len, static_cast<int>(s.d), s.dtype, st);
   }

@@ -25,6 +25,7 @@ device; one that is out of range is not used, and sync_status() then returns 7.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import NamedTuple, Optional, Tuple
 
@@ -284,12 +285,27 @@ def cache_attn(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor,
         o, lse = out
         _check_out(o, lse, q, (B, n, H, d), (B, H, n))
     shape = _abi.Shape(B, n, H, d, _dtype(q, _ATTN_TYPES), _scale(scale))
+    most = page_table.shape[1] * cache.k.shape[2]
+    if 0 < max_len < most:
+        most = max_len
+    size = _workspace_bytes(q.device.index, n, H, d, Hkv, most)
+    work = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
     _call(_abi.load().attn_jvp_cache_attn, "attn_jvp_cache_attn", q.device, ctypes.byref(shape),
           Hkv, q.data_ptr(), (ctypes.c_int64 * 3)(st[0], st[1], st[2]), ctypes.byref(desc),
           _int32(seq_lens, "seq_lens", q.device, B), _table(page_table, B, q.device),
-          page_table.shape[1], page_table.stride(0), max_len, int(causal), o.data_ptr(),
-          lse.data_ptr())
+          page_table.shape[1], page_table.stride(0), max_len, int(causal),
+          work.data_ptr() if size else None, size, o.data_ptr(), lse.data_ptr())
     return o, lse
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(device: int, n: int, H: int, d: int, Hkv: int, most: int) -> int:
+    with torch.cuda.device(device):
+        size = _abi.load().attn_jvp_cache_attn_workspace_bytes(
+            ctypes.byref(_abi.Shape(1, n, H, d, _abi.DTYPE_BF16, 0.0)), Hkv, most)
+    if size < 0:
+        raise ValueError("bad shape, or no usable device")
+    return size
 
 
 def _check_out(o, lse, q, o_shape, lse_shape):

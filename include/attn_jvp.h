@@ -605,6 +605,11 @@ int attn_jvp_cache_append(const attn_jvp_tokens* shape, const void* k, attn_jvp_
  *   max_len an upper bound of lens known on the host, or 0 for
  *           table_width * page_tokens; it sets how the work is split, and longer
  *           sequences are still computed whole
+ *   workspace  at least attn_jvp_cache_attn_workspace_bytes(shape, Hkv, m) bytes,
+ *           m being max_len, or table_width * page_tokens if that is smaller or
+ *           max_len is 0; 16-byte aligned; NULL if that is 0. Its contents
+ *           before and after the call mean nothing; calls that may overlap need
+ *           one each
  *   o       [B, n, H, d] dense, of dtype;  lse [B, H, n] float dense
  *
  * Scales in the cache are read as at least 2^-40 and at most 2^40. A sequence
@@ -614,8 +619,13 @@ int attn_jvp_cache_append(const attn_jvp_tokens* shape, const void* k, attn_jvp_
 int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, const void* q,
                         const int64_t* q_strides, const attn_jvp_cache* cache,
                         const int32_t* lens, const int32_t* table, int64_t table_width,
-                        int64_t table_stride, int64_t max_len, int32_t causal, void* o, float* lse,
-                        void* stream);
+                        int64_t table_stride, int64_t max_len, int32_t causal, void* workspace,
+                        int64_t workspace_bytes, void* o, float* lse, void* stream);
+
+/* Bytes of workspace for sequences of up to max_len tokens on the current
+ * device (0 where none is needed), or -1 on a bad argument or no device. */
+int64_t attn_jvp_cache_attn_workspace_bytes(const attn_jvp_shape* shape, int64_t Hkv,
+                                            int64_t max_len);
 
 /*
  * attn_jvp_prompt_attn - causal attention inside each of B packed sequences:

@@ -340,6 +340,40 @@ def test_cache_attn(lens, n, H, Hkv, d, page, causal, dtype, where):
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
+LONG = [  # tables of more than 4096 tokens: the steps of all sequences shared out over the blocks
+    ([4500, 33, 0, 700], 1, 8, 2, 128, 64, True, torch.bfloat16, 4600),
+    ([0, 0, 1], 1, 4, 1, 64, 16, True, torch.float16, 5000),
+    ([9001], 1, 2, 1, 128, 16, True, torch.bfloat16, 9001),
+    ([5000, 4999, 31], 4, 8, 2, 64, 128, True, torch.bfloat16, 6000),
+    ([6000, 1], 3, 15, 3, 128, 32, False, torch.float16, 6000),
+    ([(37 * i) % 100 for i in range(300)], 1, 4, 2, 64, 32, True, torch.bfloat16, 4100),
+    ([20000, 5, 4096], 1, 12, 12, 64, 64, True, torch.bfloat16, 20000),
+]
+
+
+@pytest.mark.parametrize("lens,n,H,Hkv,d,page,causal,dtype,width", LONG)
+def test_cache_attn_shared_out(lens, n, H, Hkv, d, page, causal, dtype, width):
+    g = rng(sum(lens) + n)
+    pages = sum(max(1, -(-m // page)) for m in lens) + 2
+    cache = filled(g, pages, Hkv, page, d)
+    table = tables(g, pages, lens, page, width=-(-width // page))
+    stale(cache, table, lens, page)
+    q = randn(g, len(lens), n, H, d, dtype=dtype)
+    scale = 0.8 / np.sqrt(d)
+    ref = orc.cache_attn(f64(q), f64(cache.k), f64(cache.v), f64(cache.k_scale), f64(cache.v_scale),
+                         lens, table.cpu().numpy(), causal, scale)
+    flushed = max(lens) * 448 * 2.0 ** -7 * 2.0 ** -25 * np.moveaxis(ref[4], -1, 1)[..., None]
+    o, lse = aj.cache_attn(q, cache, ints(lens), table, causal=causal, scale=scale)
+    ok()
+    check_attn(o, lse, q, ref, scale, 2.0 ** -11, flushed)
+    again = aj.cache_attn(q, cache, ints(lens), table, causal=causal, scale=scale)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    # the same sequences split within clusters
+    short = aj.cache_attn(q, cache, ints(lens), table, causal=causal, scale=scale, max_len=4096)
+    ok()
+    check_attn(*short, q, ref, scale, 2.0 ** -11, flushed)
+
+
 # ------------------------------------------------------------------ prompts
 PROMPTS = [  # (lengths, rows before, rows behind, H, Hkv, d, dtype)
     ([1], 0, 0, 1, 1, 64, torch.bfloat16),
