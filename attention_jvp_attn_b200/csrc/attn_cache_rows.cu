@@ -59,13 +59,13 @@ struct RowsParams {
 template <int D, int NT>
 struct RowsCfg {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = NT == 1 ? 2 : 3;
   static constexpr int KV = kStep * D;                // bytes of a step's keys (or values)
   static constexpr int RING = STAGES * 2 * KV;        // per warp
   static constexpr int PITCH = D + 4;                 // floats per row of a warp's sums
   static constexpr int PART = ROWS * PITCH * 4;
   static constexpr int SLOT = RING;                   // the sums lie over the ring
-  static constexpr int SCALES = STAGES * 4 * 4;       // per warp: k, v scales of the 16-token halves
+  static constexpr int SCALES = STAGES * 8 * 4;       // per warp: see `scales` below
   static constexpr int AT_WHOLE = kRowsWarps * SLOT;  // the block's sums
   static constexpr int AT_STATS = AT_WHOLE + PART;
   static constexpr int AT_SCALES = AT_STATS + (2 * kRowsWarps + 2) * ROWS * 4;
@@ -169,9 +169,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) { return Elem<__half>::pack(a, b); }
 
-__device__ __forceinline__ uint32_t lo16(uint32_t w) { return e4m3x2_to_f16x2(w & 0xffffu); }
-__device__ __forceinline__ uint32_t hi16(uint32_t w) { return e4m3x2_to_f16x2(w >> 16); }
-
 // Four columns of row r of (b, hk) from its sums.
 template <typename T, int D>
 __device__ __forceinline__ void write_row(const CacheAttnParams& p, int b, int hk, int r, int col,
@@ -194,7 +191,7 @@ __device__ __forceinline__ void fence_async() {
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __grid_constant__ RowsParams params) {
+__global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_kernel(const __grid_constant__ RowsParams params) {
   using C = RowsCfg<D, NT>;
   const CacheAttnParams& p = params.c;
   constexpr int H2 = D / 64;  // 64-column parts of the head dimension
@@ -258,13 +255,12 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
       const int j = s * kStep + (lane & 1) * 16;
       return lane < 2 && s < s_end && j < reach ? checked_page(p, b, j) : -1;
     };
-    // Copies step s, whose pages are `page`, into the next stage. Returns what
-    // lanes 0 to 3 will put into the stage's scales: keys (0, 1) and values
-    // (2, 3) of the halves, a mark for a hidden half's keys.
+    // Copies step s, whose pages are `page`, into the next stage, and reads the
+    // scales of its 16-token halves: keys in lanes 0, 1, values in lanes 2, 3.
     auto fetch = [&](int s, int page) -> float {
-      const int page0 = __shfl_sync(0xffffffffu, page, 0), page1 = __shfl_sync(0xffffffffu, page, 1);
-      float sc = lane < 2 ? __uint_as_float(kHidden) : 1.f;
+      float sc = __uint_as_float(kHidden);
       if (s < s_end) {
+        const int page0 = __shfl_sync(0xffffffffu, page, 0), page1 = __shfl_sync(0xffffffffu, page, 1);
         const int st = issued++ % C::STAGES;
         uint8_t* at = ring + st * 2 * C::KV;
         const int j = (s * kStep) & ((1 << p.page_shift) - 1);
@@ -285,6 +281,22 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
       }
       return sc;
     };
+    // Writes what the softmax needs of those into stage st's scales: for the
+    // two halves the key scales (a mark for a hidden half), log2 of the value
+    // scales, and their inverses.
+    auto keep_scales = [&](int st, float sc) {
+      if (lane < 4) {
+        const bool none = __float_as_uint(sc) == kHidden;
+        float* to = scales + 8 * st + (lane & 1);
+        const float r = none ? 1.f : read_scale(sc);
+        if (lane < 2) {
+          to[0] = none ? sc : r;
+        } else {
+          to[2] = log2_approx(r);
+          to[4] = rcp_approx(r);
+        }
+      }
+    };
 
     int next = s_begin + warp;  // next step to copy
     int page = page_of(next);
@@ -295,7 +307,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
       pending = fetch(next, page);
       next += kRowsWarps;
       page = page_of(next);
-      if (lane < 4) scales[4 * st + lane] = pending;
+      keep_scales(st, pending);
     }
 
     // Queries as fp16 fragments: k-step (h, s) holds columns (c + 4h) 16 + 4s + 0..3 of row g.
@@ -369,7 +381,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
     int late = -1;  // the stage that `pending` belongs to
     __syncwarp();
     for (int s = s_begin + warp; s < s_end; s += kRowsWarps) {
-      if (late >= 0 && lane < 4) scales[4 * late + lane] = pending;
+      if (late >= 0) keep_scales(late, pending);
       // the next stage's reads are over since the end of the last round
       late = next < s_end ? issued % C::STAGES : -1;
       pending = fetch(next, page);
@@ -381,7 +393,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
       __syncwarp();
       const uint8_t* sk = ring + stage * 2 * C::KV;
       const uint8_t* sv = sk + C::KV;
-      const float4 ss = *reinterpret_cast<const float4*>(scales + 4 * stage);
+      const float4 ss = *reinterpret_cast<const float4*>(scales + 8 * stage);
+      const float2 iv = *reinterpret_cast<const float2*>(scales + 8 * stage + 4);
 
       float x[NT][2][4];  // 16-token halves: token g (0, 1) and g + 8 (2, 3), rows 2c (0, 2), 2c + 1
 #pragma unroll
@@ -396,7 +409,9 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
           const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t a0 = lo16(us[e]), a1 = lo16(ws[e]), a2 = hi16(us[e]), a3 = hi16(ws[e]);
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(us[e], a0, a2);
+            e4m3x4_to_f16x4(ws[e], a1, a3);
 #pragma unroll
             for (int t = 0; t < NT; ++t) mma_f16(x[t][f], a0, a1, a2, a3, q[t][h][e][0], q[t][h][e][1]);
           }
@@ -404,9 +419,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
       }
       // scores in powers of two, the value scale in the exponent
       const bool hidden[2] = {__float_as_uint(ss.x) == kHidden, __float_as_uint(ss.y) == kHidden};
-      const float ks[2] = {read_scale(ss.x), read_scale(ss.y)};
-      const float vs[2] = {read_scale(ss.z), read_scale(ss.w)};
-      const float lv[2] = {log2_approx(vs[0]), log2_approx(vs[1])};
+      const float ks[2] = {ss.x, ss.y}, lv[2] = {ss.z, ss.w}, inv_v[2] = {iv.x, iv.y};
       const int j0 = s * kStep;
       const bool edge = j0 + kStep > all || hidden[0] || hidden[1];
       float top[NT][2];
@@ -460,15 +473,14 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
         const float base[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          const float inv_v = 1.f / vs[f];
           if (edge) {
             vis[t][f][0] = transpose8(pack_f16(x[t][f][0] != -INFINITY, x[t][f][1] != -INFINITY));
             vis[t][f][1] = transpose8(pack_f16(x[t][f][2] != -INFINITY, x[t][f][3] != -INFINITY));
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[t][f][e] = ajvp::ex2_approx(x[t][f][e] - base[e & 1]);
-          l[t][0] = fmaf(x[t][f][0] + x[t][f][2], inv_v, l[t][0]);
-          l[t][1] = fmaf(x[t][f][1] + x[t][f][3], inv_v, l[t][1]);
+          l[t][0] = fmaf(x[t][f][0] + x[t][f][2], inv_v[f], l[t][0]);
+          l[t][1] = fmaf(x[t][f][1] + x[t][f][3], inv_v[f], l[t][1]);
           pk[t][f][0] = transpose8(pack_f16(x[t][f][0], x[t][f][1]));
           pk[t][f][1] = transpose8(pack_f16(x[t][f][2], x[t][f][3]));
         }
@@ -499,34 +511,45 @@ __global__ void __launch_bounds__(kRowsWarps * 32) cache_rows_kernel(const __gri
         // that do not (0 * NaN). It is taken out of the product, and a second
         // product, of what each row sees and where the NaN are, says which sums
         // become NaN.
-        const bool apart = edge && __any_sync(0xffffffffu, nan);
+        if (edge && __any_sync(0xffffffffu, nan)) {
+#pragma unroll
+          for (int e = 0; e < VB / 4; ++e) {
+            uint32_t mark[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              mark[i] = (((w[i][e] & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
+              w[i][e] &= ~(mark[i] * 0xffu);
+              mark[i] *= 0x38u;  // the e4m3 code of 1
+            }
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+              const uint32_t sel = hi ? 0x7362u : 0x5140u;
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16x4(__byte_perm(mark[0], mark[1], sel), a0, a1);
+              e4m3x4_to_f16x4(__byte_perm(mark[2], mark[3], sel), a2, a3);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(hit, a0, a1, a2, a3, vis[t][f][0], vis[t][f][1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (hit[i] > 0.f) acc[t][2 * e + hi][i] = NAN;
+              }
+            }
+          }
+        }
 #pragma unroll
         for (int e = 0; e < VB / 4; ++e)
 #pragma unroll
           for (int hi = 0; hi < 2; ++hi) {
             // bytes 2hi, 2hi + 1 of the two tokens of a pair, interleaved
             const uint32_t sel = hi ? 0x7362u : 0x5140u;
-            uint32_t p0 = __byte_perm(w[0][e], w[1][e], sel), p1 = __byte_perm(w[2][e], w[3][e], sel);
-            const int j = 2 * e + hi;
-            if (apart) {
-              const uint32_t n0 = (((p0 & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
-              const uint32_t n1 = (((p1 & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
-              p0 &= ~(n0 * 0xffu);
-              p1 &= ~(n1 * 0xffu);
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(__byte_perm(w[0][e], w[1][e], sel), a0, a1);
+            e4m3x4_to_f16x4(__byte_perm(w[2][e], w[3][e], sel), a2, a3);
 #pragma unroll
-              for (int t = 0; t < NT; ++t) {
-                float hit[4] = {0.f, 0.f, 0.f, 0.f};
-                // 0x38 is the e4m3 code of 1
-                mma_f16(hit, lo16(n0 * 0x38u), hi16(n0 * 0x38u), lo16(n1 * 0x38u), hi16(n1 * 0x38u),
-                        vis[t][f][0], vis[t][f][1]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (hit[i] > 0.f) acc[t][j][i] = NAN;
-              }
-            }
-            const uint32_t a0 = lo16(p0), a1 = hi16(p0), a2 = lo16(p1), a3 = hi16(p1);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma_f16(acc[t][j], a0, a1, a2, a3, pk[t][f][0], pk[t][f][1]);
+            for (int t = 0; t < NT; ++t)
+              mma_f16(acc[t][2 * e + hi], a0, a1, a2, a3, pk[t][f][0], pk[t][f][1]);
           }
       }
       __syncwarp();
@@ -745,8 +768,8 @@ cudaError_t cache_rows_launch(const RowsParams& p, int d, int dtype, int blocks,
   return d == 128 ? rows_launch<__half, 128>(p, blocks, st) : rows_launch<__half, 64>(p, blocks, st);
 }
 
-// Blocks that share out the steps of long sequences: two per SM fit.
-constexpr int kBlocksPerSm = 2;
+// Blocks that share out the steps of long sequences: as many per SM as fit.
+constexpr int blocks_per_sm(int64_t rows) { return rows <= 8 ? 3 : 2; }
 
 // Whether sequences of up to `len` tokens are shared out over all blocks (a
 // second launch) rather than split within clusters.
@@ -767,7 +790,7 @@ extern "C" int64_t attn_jvp_cache_attn_workspace_bytes(const attn_jvp_shape* sha
   unsigned int* status = nullptr;
   int sms = 0;
   if (ajvp::device_status_word(&status, &sms) != ATTN_JVP_OK) return -1;
-  return 2 * kBlocksPerSm * int64_t(sms) * place_bytes(rows, shape->d);
+  return 2 * blocks_per_sm(rows) * int64_t(sms) * place_bytes(rows, shape->d);
 }
 
 extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, const void* q,
@@ -829,7 +852,7 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
   p.row_tiles = static_cast<int>(row_tiles);
   p.splits = 1;
   const bool share = shared_out(rows, len);
-  const int blocks = kBlocksPerSm * sms;
+  const int blocks = blocks_per_sm(rows) * sms;
   if (share) {
     if (!workspace || workspace_bytes < 2 * blocks * place_bytes(rows, s.d))
       return ATTN_JVP_ERR_INVALID_ARGUMENT;

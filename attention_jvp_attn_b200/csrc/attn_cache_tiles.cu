@@ -295,10 +295,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
             }
             uint32_t h[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              h[2 * e] = e4m3x2_to_f16x2(w[e] & 0xffffu);
-              h[2 * e + 1] = e4m3x2_to_f16x2(w[e] >> 16);
-            }
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16x4(w[e], h[2 * e], h[2 * e + 1]);
             uint8_t* row = to + k * STEP * 128;
             *reinterpret_cast<uint4*>(row + at[k % TURN][0]) = make_uint4(h[0], h[1], h[2], h[3]);
             *reinterpret_cast<uint4*>(row + at[k % TURN][1]) = make_uint4(h[4], h[5], h[6], h[7]);

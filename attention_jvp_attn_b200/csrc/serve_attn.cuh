@@ -55,6 +55,12 @@ __device__ __forceinline__ int checked_page(const CacheAttnParams& p, int b, int
   return -1;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {  // exact for powers of two
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float log2_approx(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -160,6 +160,14 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
   return r;
 }
 
+// Four codes to their values as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
+
 // The start of sequence b's rows in a packed array of T rows, from data that
 // may be out of order: always in [0, T], so that no row outside is touched.
 __device__ __forceinline__ int clamp_row(int start, int T) { return min(max(start, 0), T); }
