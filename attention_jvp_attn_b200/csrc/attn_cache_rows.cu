@@ -169,6 +169,17 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) { return Elem<__half>::pack(a, b); }
 
+// What a block of the shared-out steps leaves for the join, behind all places
+// of the workspace.
+struct Piece {
+  static constexpr int kNone = -1, kEmpty = -2;
+  int went_on;  // b Hkv + hk of a tile that an earlier block began (in its first place), or
+                // kNone, or kEmpty for a block without steps
+  int begun;    // that of a tile that it began and a later block goes on with, or kNone
+  int place;    // where the begun tile's sums are
+  int unused;
+};
+
 // Four columns of row r of (b, hk) from its sums.
 template <typename T, int D>
 __device__ __forceinline__ void write_row(const CacheAttnParams& p, int b, int hk, int r, int col,
@@ -235,6 +246,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_k
   float* scales = reinterpret_cast<float*>(smem + C::AT_SCALES + warp * C::SCALES);
   int issued = 0, taken = 0;  // steps whose copies were issued, and waited for
   bool first_piece = true;
+  Piece left = {w < w_end ? Piece::kNone : Piece::kEmpty, Piece::kNone, 0, 0};
   while (w < w_end) {
     const int len = checked_len(p, b);
     const int reach = len;  // most keys seen
@@ -626,6 +638,12 @@ __global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_k
           if (col == 0) place[C::ROWS * D + r] = top, place[C::ROWS * (D + 1) + r] = sum;
         }
       }
+      if (!whole) {
+        if (s_begin > 0)
+          left.went_on = b * p.Hkv + hk;
+        else
+          left.begun = b * p.Hkv + hk, left.place = first_piece ? 0 : 1;
+      }
       // on to the next piece, whose copies go where these sums are
       first_piece = false;
       w = base + s_end;
@@ -666,64 +684,76 @@ __global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_k
     ajvp::cluster_sync_all();  // no block leaves while its sums are read
     break;
   }
+  if (params.work && threadIdx.x == 0)
+    reinterpret_cast<Piece*>(params.work + 2 * int64_t(gridDim.x) * C::PLACE)[blockIdx.x] = left;
 }
 
-// Joins the pieces of each (sequence, key head) that was shared out over
-// several blocks; a block per (sequence, key head).
+// Joins the pieces of the (sequence, key head) that block blockIdx.x began and
+// later blocks went on with. A block takes 32 groups of 4 columns; its warps
+// take every fourth piece, four at a time, and join what they have.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kRowsWarps * 32) join_rows_kernel(const CacheAttnParams p,
                                                                     const float* work, const int blocks) {
   using C = RowsCfg<D, NT>;
+  __shared__ float stats[2][kRowsWarps][32];
+  __shared__ float4 part[kRowsWarps][32];
   cudaGridDependencySynchronize();  // launched early: the pieces are complete from here on
-  const int b = blockIdx.x / p.Hkv, hk = blockIdx.x - b * p.Hkv;
-  // its steps [g0, g1) of all
-  __shared__ int64_t sums[2][kRowsWarps];
-  int64_t before = 0, all = 0;
-  for (int i = threadIdx.x; i < p.B; i += kRowsWarps * 32) {
-    const int64_t x = int64_t(p.Hkv) * steps_of(reach_of(p, i));
-    all += x;
-    if (i < b) before += x;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if ((threadIdx.x & 31) == 0) sums[0][threadIdx.x >> 5] = all, sums[1][threadIdx.x >> 5] = before;
-  __syncthreads();
-  all = before = 0;
-#pragma unroll
-  for (int w = 0; w < kRowsWarps; ++w) all += sums[0][w], before += sums[1][w];
-  const int steps = steps_of(reach_of(p, b));
-  const int64_t g0 = before + int64_t(hk) * steps, g1 = g0 + steps;
-  // the blocks whose steps, [all k / blocks, all (k + 1) / blocks), meet them
-  int64_t k0 = g0 * blocks / all, k1 = (g1 - 1) * blocks / all;
-  while (k0 > 0 && all * k0 / blocks > g0) --k0;
-  while (all * (k0 + 1) / blocks <= g0) ++k0;
-  while (k1 > 0 && all * k1 / blocks > g1 - 1) --k1;
-  while (all * (k1 + 1) / blocks <= g1 - 1) ++k1;
-  if (k0 == k1) return;  // one block had them all
+  const Piece* pieces = reinterpret_cast<const Piece*>(work + 2 * int64_t(blocks) * C::PLACE);
+  const int first = blockIdx.x, tile = pieces[first].begun;
+  if (tile < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = blockIdx.y * 32 + lane;
+  const int r = item / (D / 4), col = (item % (D / 4)) * 4;
   const int rows = p.n * p.group;
-  for (int item = threadIdx.x; item < rows * (D / 4); item += kRowsWarps * 32) {
-    const int r = item / (D / 4), col = (item % (D / 4)) * 4;
-    // a block's first piece is in its first place
-    auto place = [&](int64_t k) { return work + (2 * k + (all * k / blocks >= g0 ? 0 : 1)) * C::PLACE; };
-    float top = -INFINITY, sum = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t k = k0; k <= k1; ++k) {
-      if (all * (k + 1) / blocks <= all * k / blocks) continue;  // a block without steps
-      top = fmaxf(top, place(k)[C::ROWS * D + r]);
+  float top = -INFINITY, sum = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float mk, float lk, const float4& z) {
+    const float to = fmaxf(top, mk);
+    const float f = to == -INFINITY ? 1.f : ajvp::ex2_approx(top - to);
+    const float g = to == -INFINITY ? 1.f : ajvp::ex2_approx(mk - to);
+    sum = sum * f + lk * g;
+    y.x = y.x * f + z.x * g, y.y = y.y * f + z.y * g;
+    y.z = y.z * f + z.z * g, y.w = y.w * f + z.w * g;
+    top = to;
+  };
+  if (warp == 0 && r < rows) {
+    const float* at = work + (2 * int64_t(first) + pieces[first].place) * C::PLACE;
+    add(at[C::ROWS * D + r], at[C::ROWS * (D + 1) + r], *reinterpret_cast<const float4*>(at + r * D + col));
+  }
+  // blocks first + 1 on, 32 at a time, until one that does not go on with the tile
+  for (int k0 = first + 1; k0 < blocks; k0 += 32) {
+    const int on = k0 + lane < blocks ? pieces[k0 + lane].went_on : -1;
+    const uint32_t ends = __ballot_sync(0xffffffffu, on != tile && on != Piece::kEmpty);
+    const uint32_t mine = __ballot_sync(0xffffffffu, on == tile);
+    const uint32_t use = ends ? mine & ((ends & -ends) - 1) : mine;
+    if (r < rows) {
+      for (int i0 = warp; i0 < 32; i0 += 4 * kRowsWarps) {
+        float mk[4], lk[4];
+        float4 z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = i0 + i * kRowsWarps;
+          mk[i] = -INFINITY, lk[i] = 0.f, z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if ((use >> j) & 1u) {
+            const float* at = work + 2 * int64_t(k0 + j) * C::PLACE;
+            mk[i] = at[C::ROWS * D + r];
+            lk[i] = at[C::ROWS * (D + 1) + r];
+            z[i] = *reinterpret_cast<const float4*>(at + r * D + col);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) add(mk[i], lk[i], z[i]);
+      }
     }
-    for (int64_t k = k0; k <= k1; ++k) {
-      if (all * (k + 1) / blocks <= all * k / blocks) continue;
-      const float* at = place(k);
-      const float f = top == -INFINITY ? 1.f : ajvp::ex2_approx(at[C::ROWS * D + r] - top);
-      const float4 z = *reinterpret_cast<const float4*>(at + r * D + col);
-      sum = fmaf(at[C::ROWS * (D + 1) + r], f, sum);
-      y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y);
-      y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
-    }
-    write_row<T, D>(p, b, hk, r, col, y, top, sum);
+    if (ends) break;
+  }
+  stats[0][warp][lane] = top, stats[1][warp][lane] = sum;
+  part[warp][lane] = y;
+  __syncthreads();
+  if (warp == 0 && r < rows) {
+#pragma unroll
+    for (int w = 1; w < kRowsWarps; ++w) add(stats[0][w][lane], stats[1][w][lane], part[w][lane]);
+    write_row<T, D>(p, tile / p.Hkv, tile % p.Hkv, r, col, y, top, sum);
   }
 }
 
@@ -746,7 +776,8 @@ cudaError_t rows_launch(const RowsParams& p, int blocks, cudaStream_t st) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, cache_rows_kernel<T, D, NT>, p);
   if (e != cudaSuccess || !p.work) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.c.B * p.c.Hkv));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks),
+                     static_cast<unsigned>((p.c.n * p.c.group * (D / 4) + 31) / 32));
   cfg.dynamicSmemBytes = 0;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -775,7 +806,10 @@ constexpr int blocks_per_sm(int64_t rows) { return rows <= 8 ? 3 : 2; }
 // second launch) rather than split within clusters.
 bool shared_out(int64_t rows, int64_t len) { return rows <= kRowsTile && len > 4096; }
 
-int64_t place_bytes(int64_t rows, int64_t d) { return (rows <= 8 ? 8 : 16) * (d + 2) * 4; }
+// Bytes of workspace per block: two places and what it leaves for the join.
+int64_t work_bytes(int64_t rows, int64_t d) {
+  return 2 * (rows <= 8 ? 8 : 16) * (d + 2) * 4 + static_cast<int64_t>(sizeof(Piece));
+}
 
 }  // namespace
 
@@ -790,7 +824,7 @@ extern "C" int64_t attn_jvp_cache_attn_workspace_bytes(const attn_jvp_shape* sha
   unsigned int* status = nullptr;
   int sms = 0;
   if (ajvp::device_status_word(&status, &sms) != ATTN_JVP_OK) return -1;
-  return 2 * blocks_per_sm(rows) * int64_t(sms) * place_bytes(rows, shape->d);
+  return blocks_per_sm(rows) * int64_t(sms) * work_bytes(rows, shape->d);
 }
 
 extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, const void* q,
@@ -854,7 +888,7 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
   const bool share = shared_out(rows, len);
   const int blocks = blocks_per_sm(rows) * sms;
   if (share) {
-    if (!workspace || workspace_bytes < 2 * blocks * place_bytes(rows, s.d))
+    if (!workspace || workspace_bytes < blocks * work_bytes(rows, s.d))
       return ATTN_JVP_ERR_INVALID_ARGUMENT;
     if (!aligned16(workspace)) return ATTN_JVP_ERR_MISALIGNED;
   }
