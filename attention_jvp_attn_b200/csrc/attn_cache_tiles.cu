@@ -11,9 +11,10 @@
 //     into the exponent; tokens come in groups of 16 of one page, so both cost
 //     a few instructions per group;
 //   - warp 8: issues the products, fp16 with fp32 sums (codes are exact);
-//   - warps 9-11: read the codes of a key tile through the page table, 16
-//     bytes at a time, and write them as fp16 into the swizzled ring that the
-//     tensor core reads.
+//   - warp 9: copies the codes of a key tile by TMA, page by page, into a stage;
+//   - warps 12-15: write them as fp16 into the swizzled ring that the tensor
+//     core reads (warps 10 and 11 do nothing: registers are given out by four
+//     warps).
 // The key tiles are split over the blocks of a cluster where the row tiles are
 // few or fill the SMs badly; the blocks join their sums through distributed
 // shared memory, so there is one launch and no workspace.
@@ -21,6 +22,8 @@
 // NaN values of tokens that some rows must not see are taken out of the
 // product and marked, as in attn_prompt.cu; a row that sees a marked token
 // gets NaN in its columns at the end.
+#include <cuda.h>
+
 #include "serve_attn.cuh"
 
 #include <type_traits>
@@ -33,10 +36,14 @@ namespace {
 
 using namespace ajvp;
 
-constexpr int kTilesThreads = 384;
-constexpr int kLoadThreads = 96;  // warps 9-11
+constexpr int kTilesThreads = 512;
 constexpr int kGroup = 16;        // tokens that share a page for certain
 constexpr int kScaleSlots = 8;    // key tiles whose scales are kept: more than the ring may run ahead
+
+struct TilesParams {
+  CUtensorMap map_k, map_v;  // codes (d, page tokens, heads, pages), boxes of a page's tokens
+  CacheAttnParams c;
+};
 
 template <int D>
 struct TilesCfg {
@@ -50,16 +57,110 @@ struct TilesCfg {
   static constexpr int SCALES = kScaleSlots * (kTile / kGroup) * 16;
   // maxima and sums of the 256 rows, at the end, behind the joined sums
   static constexpr int STATS_AT = 2 * kTile * PITCH * 4;
-  static constexpr int NBAR = 2 * NS + 4 * 2 + kScaleSlots + 2;
+  static constexpr int NBAR = 2 * NS + 5 * 2 + kScaleSlots + 2 * RAW_ONE + 2;
   static constexpr int BYTES = 1024 + DATA + SCALES + NBAR * 8 + 16 * 4 + 16;
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S_t at 128 t, O_t at 256 + D t
   static_assert(BYTES <= 232448, "shared memory budget");
   static_assert(STATS_AT + 2 * 2 * kTile * 4 <= DATA, "the joined sums lie over the tiles");
 };
 
+// The address with bits of its offset flipped (the base is aligned beyond them).
+__device__ __forceinline__ const uint8_t* smem_xor(const uint8_t* p, uint32_t bits) {
+  return reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) ^ bits);
+}
+
+// 64 scores of the lane's row.
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&s)[64]) {
+  tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+  tmem_ld32(taddr + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+  tmem_wait_ld();
+}
+
+// What the softmax needs of the four groups of 64 scores.
+struct Groups {
+  float a[4];    // score = a * product + lv, in powers of two with the value scale
+  float lv[4];   // log2 of the value scale; -inf for a group without a page
+  float inv[4];  // 1 / value scale
+  bool hidden;   // some group of the key tile has no page (the same for the whole block)
+  __device__ __forceinline__ Groups(const float4* sc, float row_scale) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float4 f = sc[g];
+      a[g] = row_scale * f.x, lv[g] = f.y, inv[g] = f.z;
+      hidden = f.w != 0.f;
+    }
+  }
+};
+
+// Scores of tokens that the row does not see, from the left-th of 64 on or in
+// a group without a page, become -inf.
+__device__ __forceinline__ void hide(uint32_t (&s)[64], Groups& gr, int left) {
+  if (left < 64) {
+#pragma unroll
+    for (int x = 0; x < 64; ++x)
+      if (x >= left) s[x] = __float_as_uint(-INFINITY);
+  }
+  if (gr.hidden) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (gr.lv[g] == -INFINITY) {
+        gr.lv[g] = 0.f;  // any finite addend will do
+#pragma unroll
+        for (int x = 0; x < kGroup; ++x) s[g * kGroup + x] = __float_as_uint(-INFINITY);
+      }
+  }
+}
+
+// Largest of 64 scores.
+__device__ __forceinline__ float max_groups(const uint32_t (&s)[64], const Groups& gr) {
+  float top[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float a = -INFINITY, c = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < kGroup; x += 4) {
+      const uint32_t* y = &s[g * kGroup + x];
+      a = fmax3(a, __uint_as_float(y[0]), __uint_as_float(y[1]));
+      c = fmax3(c, __uint_as_float(y[2]), __uint_as_float(y[3]));
+    }
+    top[g] = fmaf(fmaxf(a, c), gr.a[g], gr.lv[g]);
+  }
+  return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+
+// p = 2^(score - m) of 64 scores, packed in pairs; returns the sum of p / value
+// scale.
+__device__ __forceinline__ float exp_groups(const uint32_t (&s)[64], const Groups& gr, float m,
+                                            uint32_t (&pk)[32]) {
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float2 a2 = make_float2(gr.a[g], gr.a[g]);
+    const float2 b2 = make_float2(gr.lv[g] - base, gr.lv[g] - base);
+    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+    for (int x = 0; x < kGroup; x += 4) {
+      const uint32_t* y = &s[g * kGroup + x];
+      float2 u = __ffma2_rn(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), a2, b2);
+      float2 v = __ffma2_rn(make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), a2, b2);
+      u.x = ex2_approx(u.x), u.y = ex2_approx(u.y);
+      v.x = ex2_approx(v.x), v.y = ex2_approx(v.y);
+      sum0 = __fadd2_rn(sum0, u);
+      sum1 = __fadd2_rn(sum1, v);
+      pk[(g * kGroup + x) / 2] = pack_pair<true>(u.x, u.y);
+      pk[(g * kGroup + x) / 2 + 1] = pack_pair<true>(v.x, v.y);
+    }
+    sum0 = __fadd2_rn(sum0, sum1);
+    l = fmaf(sum0.x + sum0.y, gr.inv[g], l);
+  }
+  return l;
+}
+
 template <int D, typename T>
-__global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __grid_constant__ CacheAttnParams p) {
+__global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __grid_constant__ TilesParams params) {
   using C = TilesCfg<D>;
+  const CacheAttnParams& p = params.c;
   extern __shared__ uint8_t smem_raw[];
   // The same offset in every block of a cluster: the dynamic shared memory
   // starts at the same address in each.
@@ -67,7 +168,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + 2 * C::TILE;
-  // (key scale, log2 of the value scale, its inverse) of each group of a key tile
+  // per group of a key tile: the key scale, log2 of the value scale (-inf: no
+  // page), its inverse, and whether any group of the tile has no page
   float4* scales = reinterpret_cast<float4*>(smem + C::DATA);
   float* stats = reinterpret_cast<float*>(smem + C::STATS_AT);  // [256] maxima, [256] sums
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::DATA + C::SCALES);
@@ -75,10 +177,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
   uint64_t* empty = bars + C::NS;       // [NS] ring slot read
   uint64_t* q_full = bars + 2 * C::NS;  // [2]
   uint64_t* s_full = q_full + 2;        // [2] scores of the row tile's current key tile
-  uint64_t* p_full = q_full + 4;        // [2] its probabilities
-  uint64_t* pv_done = q_full + 6;       // [2] its sums
-  uint64_t* sc_full = q_full + 8;       // [kScaleSlots] scales of a key tile
-  uint64_t* loaded = sc_full + kScaleSlots;  // all tiles written, all marks made
+  uint64_t* p_full = q_full + 4;        // [2] its probabilities, first half
+  uint64_t* p_late = q_full + 6;        // [2] second half
+  uint64_t* pv_done = q_full + 8;       // [2] its sums
+  uint64_t* sc_full = q_full + 10;       // [kScaleSlots] scales of a key tile
+  uint64_t* raw_full = sc_full + kScaleSlots;    // [RAW_ONE] codes of a half tile landed
+  uint64_t* raw_empty = raw_full + C::RAW_ONE;   // [RAW_ONE] codes read
+  uint64_t* loaded = raw_empty + C::RAW_ONE;  // all tiles written, all marks made
   uint64_t* drain = loaded + 1;
   uint32_t* marked = reinterpret_cast<uint32_t*>(bars + C::NBAR);  // [4][4] tokens with NaN values
   uint32_t* tmem_slot = marked + 16;
@@ -107,17 +212,22 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
   };
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(&full[i], 3);
+      mbar_init(&full[i], 4);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
+      mbar_init(&p_late[i], 4);
       mbar_init(&pv_done[i], 1);
     }
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(&sc_full[i], 1);
-    mbar_init(loaded, 3);
+    for (int i = 0; i < C::RAW_ONE; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    mbar_init(loaded, 4);
     mbar_init(drain, 1);
     for (int i = 0; i < 16; ++i) marked[i] = 0;
     *abort_flag = 0;
@@ -132,7 +242,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(warp_uniform(static_cast<int>(*tmem_slot)));
 
-  if (warp >= 8) {
+  const int stages = two ? C::RAW : C::RAW_ONE;
+  auto stage_at = [&](int s) {  // the second row tile's queries' place is free without one
+    return s < C::RAW ? smem + C::RAW_AT + s * (C::TILE / 2)
+                      : sQ + C::TILE + (s - C::RAW) * (C::TILE / 2);
+  };
+
+  if (warp >= 8 && warp < 12) {
     setmaxnreg_dec<88>();
     if (warp == 8) {
       // ------------------------------------------------------------ products
@@ -162,8 +278,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
           ok = wwait(&p_full[t], j & 1);
           if (!ok) break;
           tc_fence_after();
-          mma_values<D>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi), idesc_v,
-                        j > 0);
+          mma_values_half<D, 0>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi),
+                                idesc_v, j > 0);
+          ok = wwait(&p_late[t], j & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_values_half<D, 1>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi),
+                                idesc_v, true);
           umma_commit(&pv_done[t]);
           if (j + 1 < n) scores(t, j + 1);
         }
@@ -174,145 +295,144 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
       umma_commit(drain);  // every product ends before tensor memory is released
       if (lane == 0) mbar_wait_drain(drain, 0, 1000000000ull);
       __syncwarp();
-    } else {
-      // ------------------------------------------------------------ codes to fp16
-      // Thread tid takes pieces (16 codes of a token) tid, tid + 96, ... of
-      // each tile: it copies them to its own places in a stage, some tiles
-      // ahead, and turns them into fp16 from there, so no thread waits for
-      // another's copies.
-      constexpr int Q = D / 16;  // pieces of a token's head
-      constexpr int STEP = kLoadThreads / Q;
-      const int tid = (warp - 9) * 32 + lane;
-      const int piece = tid % Q, r0 = tid / Q;
-      const uint32_t in_page = (1u << p.page_shift) - 1;
-      const uint32_t page_stride = static_cast<uint32_t>(p.page_stride);  // below 2^32: see the checks
-      const uint32_t token_stride = static_cast<uint32_t>(p.token_stride);
-      const uint8_t* k_codes = p.codes[0] + hk * p.head_stride + piece * 16;
-      const uint8_t* v_codes = p.codes[1] + hk * p.head_stride + piece * 16;
-      const int stages = two ? C::RAW : C::RAW_ONE;
-      auto stage_at = [&](int i) {  // the second row tile's queries' place is free without one
-        const int s = i % stages;
-        return (s < C::RAW ? smem + C::RAW_AT + s * (C::TILE / 2)
-                           : sQ + C::TILE + (s - C::RAW) * (C::TILE / 2)) + tid * 16;
-      };
-      // Pages of the eight groups of 16 tokens of key tile j, one per lane (-1:
-      // hidden), and in the first of the warps their scales.
-      int page = -1, page_next = -1;
-      float2 sc_next = make_float2(0.f, 0.f);
-      auto look_up = [&](int j) {
-        page_next = -1;
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ copies
+      // Half tile i is the keys (even i) or values (odd) of key tile i / 2. Its
+      // codes are copied page by page into a stage.
+      // Pages of the eight groups of 16 tokens of a key tile, one per lane. They
+      // are loaded a tile before they are used, and looked at then: -1 if hidden.
+      const int32_t* table = p.table + b * p.table_stride;
+      int raw_page = -1, page = -1;
+      auto load_page = [&](int j) {
         const int token = (j_begin + j) * kTile + lane * kGroup;
-        if (lane < kTile / kGroup && j < n && token < reach) page_next = checked_page(p, b, token);
-        if (warp == 9 && page_next >= 0) {
-          const int64_t at = page_next * p.scale_page + hk * p.scale_head;
-          sc_next = make_float2(p.scale[0][at], p.scale[1][at]);
-        }
+        raw_page = lane < kTile / kGroup && j < n && token < reach ? table[token >> p.page_shift] : -1;
       };
-      auto copy = [&](int i) {  // half tile i: keys (even) or values of key tile i / 2
-        if (i < 2 * n) {
-          if (!(i & 1)) {
-            page = page_next;
-            if (warp == 9) {
-              if (lane < kTile / kGroup) {
-                float4 s = make_float4(1.f, -INFINITY, 1.f, 0.f);  // hidden
-                if (page >= 0) {
-                  const float vs = read_scale(sc_next.y);
-                  s = make_float4(read_scale(sc_next.x), log2_approx(vs), 1.f / vs, 0.f);
-                }
-                scales[((i >> 1) % kScaleSlots) * (kTile / kGroup) + lane] = s;
-              }
-              __syncwarp();
-              mbar_arrive_if(&sc_full[(i >> 1) % kScaleSlots], lane == 0);
+      load_page(0);
+      float2 sc = make_float2(0.f, 0.f);
+      int i = 0;
+      for (; i < 2 * n; ++i) {
+        const int j = i >> 1, st = i % stages;
+        if (i & 1) {
+          // the scales, read before the keys' copies, are there by now
+          const float some = __any_sync(0xffffffffu, lane < kTile / kGroup && page < 0);
+          if (lane < kTile / kGroup) {
+            float4 f = make_float4(1.f, -INFINITY, 1.f, some);  // hidden
+            if (page >= 0) {
+              const float vs = read_scale(sc.y);
+              f = make_float4(read_scale(sc.x), log2_approx(vs), rcp_approx(vs), some);
             }
-            look_up((i >> 1) + 1);
+            scales[(j % kScaleSlots) * (kTile / kGroup) + lane] = f;
           }
-          const uint8_t* src = (i & 1) ? v_codes : k_codes;
-          const uint32_t dst = smem_u32(stage_at(i));
-          const int left = reach - (j_begin + (i >> 1)) * kTile;  // tokens from the tile's first on
-#pragma unroll
-          for (int k = 0; k * STEP < kTile; ++k) {
-            const int r = r0 + k * STEP;
-            const int pg = __shfl_sync(0xffffffffu, page, (r / kGroup) & 31);
-            if ((k + 1) * STEP <= kTile || r < kTile) {
-              const bool valid = pg >= 0 && r < left;
-              const uint32_t pr = valid ? pg : 0;
-              copy16(dst + k * kLoadThreads * 16,
-                     src + uint64_t(pr) * page_stride + uint64_t(uint32_t(r) & in_page) * token_stride,
-                     valid);
-            }
+          __syncwarp();
+          mbar_arrive_if(&sc_full[j % kScaleSlots], lane == 0);
+        } else {
+          const int token = (j_begin + j) * kTile + lane * kGroup;
+          page = raw_page >= 0 && raw_page < p.pages ? raw_page : -1;
+          if (page < 0 && lane < kTile / kGroup && token < reach) atomicOr(p.status, kStatusBadIndex);
+          if (page >= 0) {
+            const int64_t at = page * p.scale_page + hk * p.scale_head;
+            sc = make_float2(p.scale[0][at], p.scale[1][at]);
           }
+          load_page(j + 1);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
-      // Where a piece's two 16-byte columns go in the swizzled tile, from its
-      // row block on: rows 12 apart (d = 128) take two placings in turn.
-      constexpr int COUNT = (kTile + STEP - 1) / STEP;  // pieces of a thread
-      constexpr int BATCH = 6;
-      constexpr int TURN = STEP % 8 ? 2 : 1;
-      static_assert(TURN * STEP % 8 == 0, "the swizzle repeats every 8 rows");
-      int at[TURN][2];
-#pragma unroll
-      for (int x = 0; x < TURN; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          at[x][y] = (piece >> 2) * kTile * 128 + r0 * 128 +
-                     ((((piece & 3) * 2 + y) ^ ((r0 + x * STEP) & 7)) << 4);
-      look_up(0);
-      for (int i = 0; i < stages; ++i) copy(i);
-      for (int i = 0; i < 2 * n; ++i) {
-        const int slot = i % C::NS;
-        if (stages == C::RAW)
-          asm volatile("cp.async.wait_group %0;" ::"n"(C::RAW - 1) : "memory");
-        else
-          asm volatile("cp.async.wait_group %0;" ::"n"(C::RAW_ONE - 1) : "memory");
-        if (!wwait(&empty[slot], ((i / C::NS) & 1) ^ 1)) break;
-        const int j = j_begin + (i >> 1);
-        const uint8_t* from = stage_at(i);
-        uint8_t* to = sRing + slot * C::TILE;
-        const bool look = (i & 1) && j >= first_edge;
-#pragma unroll
-        for (int k0 = 0; k0 < COUNT; k0 += BATCH) {
-          // a batch of pieces is read before the first is written: the
-          // compiler cannot tell the two places apart
-          uint4 u[BATCH];
-#pragma unroll
-          for (int k = k0; k < k0 + BATCH && k < COUNT; ++k)
-            u[k - k0] = *reinterpret_cast<const uint4*>(from + k * kLoadThreads * 16);
-#pragma unroll
-          for (int k = k0; k < k0 + BATCH && k < COUNT; ++k) {
-            if ((k + 1) * STEP > kTile && r0 + k * STEP >= kTile) continue;
-            uint32_t w[4] = {u[k - k0].x, u[k - k0].y, u[k - k0].z, u[k - k0].w};
-            if (look) {
-              bool nan = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t m = (((w[e] & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
-                nan |= m != 0;
-                w[e] &= ~(m * 0xffu);
-              }
-              const int r = r0 + k * STEP;
-              if (nan) atomicOr(&marked[4 * (j - first_edge) + (r >> 5)], 1u << (r & 31));
-            }
-            uint32_t h[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) e4m3x4_to_f16x4(w[e], h[2 * e], h[2 * e + 1]);
-            uint8_t* row = to + k * STEP * 128;
-            *reinterpret_cast<uint4*>(row + at[k % TURN][0]) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(row + at[k % TURN][1]) = make_uint4(h[4], h[5], h[6], h[7]);
-          }
-        }
-        fence_proxy_async_shared();
+        if (!wwait(&raw_empty[st], ((i / stages) & 1) ^ 1)) break;
+        const bool box = page >= 0 && ((lane * kGroup) & ((1 << p.page_shift) - 1)) == 0;
+        const int boxes = __popc(__ballot_sync(0xffffffffu, box));
+        if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], boxes * (D << p.page_shift));
         __syncwarp();
-        mbar_arrive_if(&full[slot], lane == 0);
-        copy(i + stages);
+        if (box)
+          tma_load_4d(stage_at(st) + lane * kGroup * D, (i & 1) ? &params.map_v : &params.map_k,
+                      &raw_full[st], 0, 0, hk, page);
+        __syncwarp();
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncwarp();
-      mbar_arrive_if(loaded, lane == 0);
+      // after an abort: every copy issued lands before the block ends
+      if (i < 2 * n)
+        for (int k = max(i - stages, 0); k < i; ++k)
+          mbar_wait_drain(&raw_full[k % stages], (k / stages) & 1, 200000000ull);
     }
+  } else if (warp >= 12) {
+    setmaxnreg_dec<96>();
+    // -------------------------------------------------------------- codes to fp16
+    // Each lane takes 16 codes of a token at a time. A quarter warp takes four
+    // adjacent ones of two rows whose places differ in bits 0 and 2, which puts
+    // its reads (of rows swizzled by the copies) and its writes (of the ring's
+    // swizzled rows) on all banks; a warp takes 8 rows at a time.
+    constexpr int CH = D / 64;            // 64-column parts
+    constexpr int COUNT = 4 * CH;         // pieces of a lane: 16 blocks of 8 rows, 4 warps
+    const int r7 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), q = lane & 3;
+    const int from_at = D == 128 ? r7 * 128 + ((q ^ r7) << 4) : r7 * 64 + ((q ^ ((r7 >> 1) & 3)) << 4);
+    const int to_lo = r7 * 128 + (((2 * q) ^ r7) << 4), to_hi = r7 * 128 + (((2 * q + 1) ^ r7) << 4);
+    uint32_t hidden = 0;  // groups of the key tile without a page
+    for (int i = 0; i < 2 * n; ++i) {
+      const int slot = i % C::NS, st = i % stages, j = j_begin + (i >> 1);
+      if (!(i & 1)) {
+        const int k = (i >> 1) % kScaleSlots;
+        if (!wwait(&sc_full[k], ((i >> 1) / kScaleSlots) & 1)) break;
+        hidden = __ballot_sync(0xffffffffu,
+                               lane < kTile / kGroup &&
+                                   scales[k * (kTile / kGroup) + lane % (kTile / kGroup)].y == -INFINITY);
+      }
+      if (!wwait(&raw_full[st], (i / stages) & 1)) break;
+      const uint8_t* from = stage_at(st) + from_at;
+      // all pieces are read before the first is written: the compiler cannot
+      // tell the two places apart
+      uint4 u[COUNT];
+#pragma unroll
+      for (int k = 0; k < COUNT; ++k) {
+        const int block = (k / CH) * 4 + warp - 12;
+        // the second part of a 128-byte row: chunk 4 + q, so bit 2 of its place
+        u[k] = *reinterpret_cast<const uint4*>(D == 128 ? smem_xor(from + block * 1024, (k % CH) << 6)
+                                                        : from + block * 512);
+      }
+      __syncwarp();
+      mbar_arrive_if(&raw_empty[st], lane == 0);
+      // tokens that nobody sees, or without a page, become zeros
+      const int left = reach - j * kTile;
+      if (left < kTile || hidden != 0) {
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k) {
+          const int r = ((k / CH) * 4 + warp - 12) * 8 + r7;
+          if (r >= left || ((hidden >> (r / kGroup)) & 1u)) u[k] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if ((i & 1) && j >= first_edge) {
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k) {
+          const int r = ((k / CH) * 4 + warp - 12) * 8 + r7;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&u[k]);
+          bool nan = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t m = (((w[e] & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
+            nan |= m != 0;
+            w[e] &= ~(m * 0xffu);
+          }
+          if (nan) atomicOr(&marked[4 * (j - first_edge) + (r >> 5)], 1u << (r & 31));
+        }
+      }
+      if (!wwait(&empty[slot], ((i / C::NS) & 1) ^ 1)) break;
+      uint8_t* to = sRing + slot * C::TILE;
+#pragma unroll
+      for (int k = 0; k < COUNT; ++k) {
+        const int block = (k / CH) * 4 + warp - 12;
+        uint32_t h[8];
+        e4m3x4_to_f16x4(u[k].x, h[0], h[1]);
+        e4m3x4_to_f16x4(u[k].y, h[2], h[3]);
+        e4m3x4_to_f16x4(u[k].z, h[4], h[5]);
+        e4m3x4_to_f16x4(u[k].w, h[6], h[7]);
+        uint8_t* part = to + (k % CH) * kTile * 128 + block * 1024;
+        *reinterpret_cast<uint4*>(part + to_lo) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(part + to_hi) = make_uint4(h[4], h[5], h[6], h[7]);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      mbar_arrive_if(&full[slot], lane == 0);
+    }
+    __syncwarp();
+    mbar_arrive_if(loaded, lane == 0);
   } else {
     // ------------------------------------------------------------ softmax
-    setmaxnreg_inc<208>();
+    setmaxnreg_inc<160>();
     const int t = warp >> 2, sub = warp & 3;
     const int row = sub * 32 + lane;
     const int r = row0 + t * kTile + row;  // row of the key head
@@ -371,74 +491,47 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
         break;
       }
       tc_fence_after();
-      uint32_t s[kTile];
-#pragma unroll
-      for (int x = 0; x < kTile; x += 32)
-        tmem_ld32(tS + x, *reinterpret_cast<uint32_t(*)[32]>(&s[x]));
-      tmem_wait_ld();
       const float4* sc = scales + (j % kScaleSlots) * (kTile / kGroup);
-      const int k0 = (j_begin + j) * kTile;
-      if (j_begin + j >= first_edge) {
-        const int left = seen - k0;
-#pragma unroll
-        for (int x = 0; x < kTile; ++x)
-          if (x >= left) s[x] = __float_as_uint(-INFINITY);
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int g = 0; g < kTile / kGroup; ++g) {
-        const float4 f = sc[g];
-        if (f.y == -INFINITY) {  // a hidden group: the same for the whole block
-#pragma unroll
-          for (int x = 0; x < kGroup; ++x) s[g * kGroup + x] = __float_as_uint(-INFINITY);
-        }
-        float a = -INFINITY, c = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < kGroup; x += 4) {
-          const uint32_t* y = &s[g * kGroup + x];
-          a = fmax3(a, __uint_as_float(y[0]), __uint_as_float(y[1]));
-          c = fmax3(c, __uint_as_float(y[2]), __uint_as_float(y[3]));
-        }
-        top = fmaxf(top, fmaf(fmaxf(a, c), row_scale * f.x, f.y));
-      }
+      const int left = j_begin + j >= first_edge ? seen - (j_begin + j) * kTile : kTile;
+      // As in attn_prompt.cu: the first half's probabilities are formed at the
+      // running maximum while the row's largest score is being found, and
+      // again only if that is much larger. The scores stay in tensor memory
+      // until then, and 64 at a time in registers.
+      uint32_t s[64], pk[32];
+      float top, add;
+      load_scores(tS, s);
+      Groups gr(sc, row_scale);
+      hide(s, gr, left);
+      top = max_groups(s, gr);
+      add = exp_groups(s, gr, m, pk);
+      load_scores(tS + 64, s);
+      Groups late(sc + 4, row_scale);
+      hide(s, late, left - 64);
+      top = fmaxf(top, max_groups(s, late));
       if (__any_sync(0xffffffffu, top > m + kLazyMax)) {
         const float to = fmaxf(m, top);
         const float f = to == -INFINITY ? 1.f : ex2_approx(m - to);
         m = to;
         l *= f;
         if (j > 0) rescale_sums<D>(tO, f);
+        load_scores(tS, s);
+        gr = Groups(sc, row_scale);
+        hide(s, gr, left);
+        add = exp_groups(s, gr, m, pk);
+        load_scores(tS + 64, s);
+        late = Groups(sc + 4, row_scale);
+        hide(s, late, left - 64);
       }
-      const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float4 f = sc[4 * h + g];
-          const float2 a2 = make_float2(row_scale * f.x, row_scale * f.x);
-          // a hidden group has scores of -inf and any finite addend
-          const float add = f.y == -INFINITY ? 0.f : f.y - base;
-          const float2 b2 = make_float2(add, add);
-          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-          for (int x = 0; x < kGroup; x += 4) {
-            const uint32_t* y = &s[(4 * h + g) * kGroup + x];
-            float2 u = __ffma2_rn(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), a2, b2);
-            float2 v = __ffma2_rn(make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), a2, b2);
-            u.x = ex2_approx(u.x), u.y = ex2_approx(u.y);
-            v.x = ex2_approx(v.x), v.y = ex2_approx(v.y);
-            sum0 = __fadd2_rn(sum0, u);
-            sum1 = __fadd2_rn(sum1, v);
-            pk[(g * kGroup + x) / 2] = pack_pair<true>(u.x, u.y);
-            pk[(g * kGroup + x) / 2 + 1] = pack_pair<true>(v.x, v.y);
-          }
-          l = fmaf((sum0.x + sum0.y) + (sum1.x + sum1.y), f.z, l);
-        }
-        tmem_st32(tS + 32 * h, pk);
-      }
+      tmem_st32(tS, pk);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive_if(&p_full[t], lane == 0);
+      add += exp_groups(s, late, m, pk);
+      tmem_st32(tS + 32, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive_if(&p_late[t], lane == 0);
+      l += add;
     }
     // ---------------------------------------------------------- sums
     ok = ok && active && (n == 0 || wwait(&pv_done[t], (n - 1) & 1)) && wwait(loaded, 0);
@@ -577,7 +670,8 @@ struct TilesKernel {
     }
     return cudaSuccess;
   }
-  static cudaError_t launch(CacheAttnParams& p, int64_t keys, cudaStream_t st) {
+  static cudaError_t launch(TilesParams& params, int64_t keys, cudaStream_t st) {
+    CacheAttnParams& p = params.c;
     // The number of splits that ends first, in key tiles per block and round
     // of the clusters that run at once: clusters above 2 leave some SMs out
     // (15 clusters of 8 fit, but 74 of 2). A block takes about 2 tiles' time to
@@ -597,18 +691,26 @@ struct TilesKernel {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     config(&cfg, &attr, p.B * p.Hkv * p.row_tiles * p.splits, p.splits, st);
-    return cudaLaunchKernelEx(&cfg, cache_tiles_kernel<D, T>, p);
+    return cudaLaunchKernelEx(&cfg, cache_tiles_kernel<D, T>, params);
   }
 };
 
 }  // namespace
 
-cudaError_t cache_tiles_launch(CacheAttnParams& p, int64_t keys, int d, int dtype, cudaStream_t st) {
+cudaError_t cache_tiles_launch(const CacheAttnParams& p, int64_t keys, int d, int dtype, cudaStream_t st) {
+  TilesParams t;
+  t.c = p;
+  const int page = 1 << p.page_shift;
+  if (!encode_cache_map(&t.map_k, p.codes[0], d, page, p.Hkv, p.pages, p.token_stride, p.head_stride,
+                        p.page_stride, page) ||
+      !encode_cache_map(&t.map_v, p.codes[1], d, page, p.Hkv, p.pages, p.token_stride, p.head_stride,
+                        p.page_stride, page))
+    return cudaErrorInvalidValue;
   if (dtype == ATTN_JVP_BF16)
-    return d == 128 ? TilesKernel<128, __nv_bfloat16>::launch(p, keys, st)
-                    : TilesKernel<64, __nv_bfloat16>::launch(p, keys, st);
-  return d == 128 ? TilesKernel<128, __half>::launch(p, keys, st)
-                  : TilesKernel<64, __half>::launch(p, keys, st);
+    return d == 128 ? TilesKernel<128, __nv_bfloat16>::launch(t, keys, st)
+                    : TilesKernel<64, __nv_bfloat16>::launch(t, keys, st);
+  return d == 128 ? TilesKernel<128, __half>::launch(t, keys, st)
+                  : TilesKernel<64, __half>::launch(t, keys, st);
 }
 
 }  // namespace ajvp_serve

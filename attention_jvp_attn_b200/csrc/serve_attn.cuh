@@ -67,13 +67,6 @@ __device__ __forceinline__ float log2_approx(float x) {
   return y;
 }
 
-// Asynchronous copy of 16 bytes to shared memory, zeros if not `valid`.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-
 // Another block's shared memory.
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
@@ -91,9 +84,9 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 }
 
 constexpr int kRowsTile = 16;  // most query rows per key head of attn_cache_rows.cu
-// attn_cache_tiles.cu: pairs of tiles of 128 query rows on tcgen05; sets p.splits
-// for sequences of up to `keys` tokens
-cudaError_t cache_tiles_launch(CacheAttnParams& p, int64_t keys, int d, int dtype, cudaStream_t st);
+// attn_cache_tiles.cu: pairs of tiles of 128 query rows on tcgen05, split for
+// sequences of up to `keys` tokens
+cudaError_t cache_tiles_launch(const CacheAttnParams& p, int64_t keys, int d, int dtype, cudaStream_t st);
 constexpr int kTilesRows = 256;
 
 }  // namespace ajvp_serve

@@ -40,13 +40,6 @@ __device__ __forceinline__ void mma_values_half(uint32_t d_tmem, uint32_t a_tmem
                   (accumulate || ks > 4 * HALF) ? 1u : 0u);
 }
 
-template <int D>
-__device__ __forceinline__ void mma_values(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_smem,
-                                           uint32_t idesc, bool accumulate) {
-  mma_values_half<D, 0>(d_tmem, a_tmem, b_smem, idesc, accumulate);
-  mma_values_half<D, 1>(d_tmem, a_tmem, b_smem, idesc, true);
-}
-
 // 3-D tiled load, as tma_load_4d_hint.
 __device__ __forceinline__ void tma_load_3d_hint(void* smem_dst, const void* map, uint64_t* bar,
                                                  int c0, int c1, int c2, uint64_t policy) {
