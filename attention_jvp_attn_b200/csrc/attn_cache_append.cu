@@ -11,13 +11,12 @@
 // e4m3 is a floating-point format; a free scale would gain at most one bit of
 // range at its lower end.
 //
-// One block per (page that gets tokens, head, K or V): it alone reads and
-// writes that page's codes and scale, so no atomics and no second launch are
-// needed. Each thread holds its values in registers between the maximum and
-// the rounding: one read of the input, one write of the codes. Bound by HBM
-// for prompts, by latency for single tokens.
-#include "serve_common.cuh"
-#include "rope_math.cuh"
+// One block takes a (page that gets tokens, head, K or V) and some more: it alone
+// reads and writes that page's codes and scale, so no atomics and no second
+// launch are needed. Each thread holds its values in registers between the
+// maximum and the rounding: one read of the input, one write of the codes.
+// Bound by HBM for prompts, by latency for single tokens.
+#include "rope_slots.cuh"
 
 namespace ajvp_serve {
 
@@ -36,57 +35,25 @@ struct AppendParams {
   const float* cos;  // null: no rotation
   const float* sin;
   unsigned int* status;
-  int T, B, pages, table_width, n_positions;
+  int T, B, heads, pages, table_width, n_positions;
   int d, half, half_layout;
 };
 
-// Eight rotated (K) or plain (V) values of one token's head, at column col.
-template <typename T>
-__device__ __forceinline__ void append_values(const AppendParams& p, const T* row, int col, bool turn,
-                                              int64_t pos, float (&x)[8]) {
-  load8(row + col, x);
-  if (!turn || col >= 2 * p.half) return;
-  const float* cp = p.cos + pos * p.half;
-  const float* sp = p.sin + pos * p.half;
-  if (!p.half_layout) {
-    float c[4], s[4];
-    load4(cp + col / 2, c);
-    load4(sp + col / 2, s);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ajvp::rope_rotate_pair(x[2 * i], x[2 * i + 1], c[i], s[i]);
-    return;
-  }
-  // The other half of each pair is read too (by the thread that owns it as
-  // well: from L1), and the half of the result that belongs here is kept.
-  const bool upper = col >= p.half;
-  const int at = upper ? col - p.half : col;
-  float y[8], c[8], s[8];
-  load8(row + (upper ? at : at + p.half), y);
-  load4(cp + at, reinterpret_cast<float(&)[4]>(c[0]));
-  load4(cp + at + 4, reinterpret_cast<float(&)[4]>(c[4]));
-  load4(sp + at, reinterpret_cast<float(&)[4]>(s[0]));
-  load4(sp + at + 4, reinterpret_cast<float(&)[4]>(s[4]));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float a = upper ? y[i] : x[i], b = upper ? x[i] : y[i];
-    ajvp::rope_rotate_pair(a, b, c[i], s[i]);
-    x[i] = upper ? b : a;
-  }
-}
-
-// PER: groups of 8 values per thread, page_tokens * d / 8 / THREADS.
-template <typename T, int PER, int THREADS>
-__global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ AppendParams p,
-                                                         const int page_tokens) {
-  __shared__ float red[THREADS / 32];
-  const int which = blockIdx.z, head = blockIdx.y;
+// A block takes the new tokens of one page, for UN units (head, K or V) at
+// once: the loads of all are in flight together behind one look-up of the
+// page. PER: slots of 16 values of a unit per thread (rope_slots.cuh).
+template <typename T, int D, int PER, int UN, int THREADS>
+__global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int per_row = D / 16;
+  constexpr int page_tokens = PER * THREADS / per_row;
+  __shared__ float red[UN][THREADS / 32];
   const int b = find_sequence(p.starts, p.B, p.T, page_tokens, 2, blockIdx.x);
   const int raw0 = p.starts[b], raw1 = p.starts[b + 1];
+  const int old = p.cached[b];
   const int t0 = clamp_row(raw0, p.T), t1 = clamp_row(raw1, p.T);
   const int piece = static_cast<int>(blockIdx.x - (t0 / page_tokens + 2ll * b));
   if (threadIdx.x == 0 && (t0 != raw0 || t1 != raw1 || t1 < t0))
     atomicOr(p.status, kStatusBadIndex);
-  const int old = p.cached[b];
   if (t1 <= t0 || piece < 0) return;
   if (old < 0) {
     if (threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
@@ -103,82 +70,129 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
     if (threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
     return;
   }
-  const T* in = static_cast<const T*>(p.in[which]) + head * p.in_head[which];
-  uint8_t* codes = p.codes[which] + page * p.page_stride + head * p.head_stride;
-  float* scale = p.scale[which] + page * p.scale_page + head * p.scale_head;
-  const float before = lo > 0 ? *scale : 0.f;
-  const int per_row = p.d / 8;
-  float x[PER][8];
-  float amax = 0.f;
+  const int unit0 = blockIdx.y * UN, units = 2 * p.heads;
+  float x[UN][PER][16], amax[UN], before[UN];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int g = i * THREADS + threadIdx.x;
-    const int row = g / per_row, col = (g - row * per_row) * 8;
-    if (row >= lo && row < hi) {
-      const int64_t pos = first + row;
-      append_values(p, in + (t0 + pos - old) * p.in_token[which], col, which == 0 && p.cos, pos,
-                    x[i]);
+  for (int u = 0; u < UN; ++u) {
+    const int which = unit0 + u >= p.heads ? 1 : 0, head = unit0 + u - which * p.heads;
+    const bool has = unit0 + u < units;
+    before[u] = 0.f;
+    if (has && lo > 0) before[u] = p.scale[which][page * p.scale_page + head * p.scale_head];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = fabsf(x[i][j]);
-        amax = fmaxf(amax, a < INFINITY ? a : 0.f);  // a NaN compares false
+    for (int i = 0; i < PER; ++i) {
+      const int g = i * THREADS + threadIdx.x;
+      const int row = g / per_row;
+      float (&a)[8] = reinterpret_cast<float(&)[8]>(x[u][i][0]);
+      float (&c)[8] = reinterpret_cast<float(&)[8]>(x[u][i][8]);
+      if (has && row >= lo && row < hi) {
+        const RopeSlot sl(g % per_row, which ? 0 : p.half, p.half_layout);
+        const int64_t pos = first + row;
+        load_slot(static_cast<const T*>(p.in[which]) + head * p.in_head[which] +
+                      (t0 + pos - old) * p.in_token[which],
+                  sl, a, c);
+        if (sl.pair >= 0) {
+          float co[8], si[8];
+          load_turn(p.cos, p.sin, pos, p.half, sl, co, si);
+          turn_slot(sl.split, a, c, co, si);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[u][i][j] = 0.f;
       }
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+  for (int u = 0; u < UN; ++u) {
+    amax[u] = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) amax[u] = fmaxf(amax[u], fabsf(x[u][i][j]));  // a NaN is passed over
+    if (amax[u] == INFINITY) {  // once more, without infinities
+      amax[u] = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float a = fabsf(x[u][i][j]);
+          amax[u] = fmaxf(amax[u], a < INFINITY ? a : 0.f);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      amax[u] = fmaxf(amax[u], __shfl_xor_sync(0xffffffffu, amax[u], o));
+    if ((threadIdx.x & 31) == 0) red[u][threadIdx.x >> 5] = amax[u];
+  }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) amax = fmaxf(amax, red[w]);
-  // amax = m 2^e with 0.5 <= m < 1, and 448 = 0.875 * 2^9
-  int e = kMinExp;
-  if (amax > 0.f) {
-    const float m = frexpf(amax, &e);
-    e = min(max(e - 9 + (m > 0.875f ? 1 : 0), kMinExp), kMaxExp);
-  }
-  const float fresh = ldexpf(1.f, e);
-  const float after = fmaxf(fresh, before);
-  const float inv = 1.f / after;  // exact for powers of two
+  for (int u = 0; u < UN; ++u) {
+    if (unit0 + u >= units) break;
+    const int which = unit0 + u >= p.heads ? 1 : 0, head = unit0 + u - which * p.heads;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int g = i * THREADS + threadIdx.x;
-    const int row = g / per_row, col = (g - row * per_row) * 8;
-    if (row >= hi) continue;
-    uint2* at = reinterpret_cast<uint2*>(codes + row * p.token_stride + col);
-    if (row >= lo) {
-      uint2 r;
-      r.x = e4m3x2(x[i][0] * inv, x[i][1] * inv) | (e4m3x2(x[i][2] * inv, x[i][3] * inv) << 16);
-      r.y = e4m3x2(x[i][4] * inv, x[i][5] * inv) | (e4m3x2(x[i][6] * inv, x[i][7] * inv) << 16);
-      *at = r;
-    } else if (after != before) {  // an earlier token, to the larger scale
-      const float ratio = before * inv;
-      uint2 r = *at;
-      uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+    for (int w = 0; w < THREADS / 32; ++w) amax[u] = fmaxf(amax[u], red[u][w]);
+    // amax = f 2^E with 1 <= f < 2, and 448 = 1.75 * 2^8 (a subnormal amax is
+    // below the smallest scale anyway)
+    const uint32_t bits = __float_as_uint(amax[u]);
+    const int e = min(max(static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0),
+                          kMinExp), kMaxExp);
+    const float fresh = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    const float after = fmaxf(fresh, before[u]);
+    const float inv = after == fresh ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f / after;
+    uint8_t* codes = p.codes[which] + page * p.page_stride + head * p.head_stride;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float a, c, f, h;
-        Elem<__half>::unpack(e4m3x2_to_f16x2(w[j] & 0xffffu), a, c);
-        Elem<__half>::unpack(e4m3x2_to_f16x2(w[j] >> 16), f, h);
-        w[j] = e4m3x2(a * ratio, c * ratio) | (e4m3x2(f * ratio, h * ratio) << 16);
+    for (int i = 0; i < PER; ++i) {
+      const int g = i * THREADS + threadIdx.x;
+      const int row = g / per_row;
+      if (row >= hi) continue;
+      const RopeSlot sl(g % per_row, which ? 0 : p.half, p.half_layout);
+      uint8_t* at = codes + row * p.token_stride;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint2* to = reinterpret_cast<uint2*>(at + (k ? sl.c1 : sl.c0));
+        if (row >= lo) {
+          const float* y = &x[u][i][8 * k];
+          uint2 r;
+          r.x = e4m3x2(y[0] * inv, y[1] * inv) | (e4m3x2(y[2] * inv, y[3] * inv) << 16);
+          r.y = e4m3x2(y[4] * inv, y[5] * inv) | (e4m3x2(y[6] * inv, y[7] * inv) << 16);
+          *to = r;
+        } else if (after != before[u]) {  // an earlier token, to the larger scale
+          const float ratio = before[u] * inv;
+          uint2 r = *to;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float a, c, f, h;
+            Elem<__half>::unpack(e4m3x2_to_f16x2(w[j] & 0xffffu), a, c);
+            Elem<__half>::unpack(e4m3x2_to_f16x2(w[j] >> 16), f, h);
+            w[j] = e4m3x2(a * ratio, c * ratio) | (e4m3x2(f * ratio, h * ratio) << 16);
+          }
+          *to = r;
+        }
       }
-      *at = r;
     }
+    if (threadIdx.x == 0) p.scale[which][page * p.scale_page + head * p.scale_head] = after;
   }
-  if (threadIdx.x == 0) *scale = after;
 }
 
-// A page's values over the block: 8 values a thread (128 to 256 threads) up
-// to pages of 2048 values, then more per thread.
-template <typename T>
-void append_launch(const AppendParams& p, int page_tokens, dim3 grid, cudaStream_t st) {
-  switch (page_tokens * p.d / 8) {
-    case 128: append_kernel<T, 1, 128><<<grid, 128, 0, st>>>(p, page_tokens); break;
-    case 256: append_kernel<T, 1, 256><<<grid, 256, 0, st>>>(p, page_tokens); break;
-    case 512: append_kernel<T, 2, 256><<<grid, 256, 0, st>>>(p, page_tokens); break;
-    case 1024: append_kernel<T, 4, 256><<<grid, 256, 0, st>>>(p, page_tokens); break;
-    default: append_kernel<T, 8, 256><<<grid, 256, 0, st>>>(p, page_tokens); break;
+// 32 values a thread in flight (64 for the largest pages), whatever the page.
+template <typename T, int D>
+void append_launch(const AppendParams& p, int page_tokens, int pieces, cudaStream_t st) {
+  constexpr int R = D / 64;  // 1 or 2
+  auto grid = [&](int un) { return dim3(pieces, (2 * p.heads + un - 1) / un); };
+  switch (page_tokens) {
+    case 16: append_kernel<T, D, 1, 2, 64 * R><<<grid(2), 64 * R, 0, st>>>(p); break;
+    case 32: append_kernel<T, D, 1, 2, 128 * R><<<grid(2), 128 * R, 0, st>>>(p); break;
+    case 64: append_kernel<T, D, R, 2 / R, 256><<<grid(2 / R), 256, 0, st>>>(p); break;
+    default: append_kernel<T, D, 2 * R, 1, 256><<<grid(1), 256, 0, st>>>(p); break;
   }
+}
+
+template <typename T>
+void append_launch(const AppendParams& p, int page_tokens, int pieces, cudaStream_t st) {
+  if (p.d == 128)
+    append_launch<T, 128>(p, page_tokens, pieces, st);
+  else
+    append_launch<T, 64>(p, page_tokens, pieces, st);
 }
 
 }  // namespace ajvp_serve
@@ -225,15 +239,15 @@ extern "C" int attn_jvp_cache_append(const attn_jvp_tokens* shape, const void* k
   p.half_layout = rope && rope->layout == ATTN_JVP_ROPE_HALF;
   p.T = static_cast<int>(s.T), p.B = static_cast<int>(B);
   p.pages = static_cast<int>(cache->pages), p.table_width = static_cast<int>(table_width);
-  p.d = static_cast<int>(s.d);
+  p.d = static_cast<int>(s.d), p.heads = static_cast<int>(s.Hkv);
   const int page = static_cast<int>(cache->page_tokens);
-  const dim3 grid(static_cast<unsigned>(s.T / page + 2 * B), static_cast<unsigned>(s.Hkv), 2);
+  const int pieces = static_cast<int>(s.T / page + 2 * B);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s.dtype == ATTN_JVP_BF16)
-    append_launch<__nv_bfloat16>(p, page, grid, st);
+    append_launch<__nv_bfloat16>(p, page, pieces, st);
   else if (s.dtype == ATTN_JVP_F16)
-    append_launch<__half>(p, page, grid, st);
+    append_launch<__half>(p, page, pieces, st);
   else
-    append_launch<float>(p, page, grid, st);
+    append_launch<float>(p, page, pieces, st);
   return cudaGetLastError() == cudaSuccess ? ATTN_JVP_OK : ATTN_JVP_ERR_CUDA;
 }

@@ -273,14 +273,15 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
       if (ok) umma_commit(&empty[0]);
       for (int j = 0; ok && j < n; ++j) {
         const int vi = 2 * j + 1, ki = 2 * j + 2;
-        ok = landed(vi) && (j + 1 == n || landed(ki));
+        ok = landed(vi);
         for (int t = 0; ok && t < nt; ++t) {
           ok = wwait(&p_full[t], j & 1);
           if (!ok) break;
           tc_fence_after();
           mma_values_half<D, 0>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi),
                                 idesc_v, j > 0);
-          ok = wwait(&p_late[t], j & 1);
+          if (t == 0 && j + 1 < n) ok = landed(ki);
+          ok = ok && wwait(&p_late[t], j & 1);
           if (!ok) break;
           tc_fence_after();
           mma_values_half<D, 1>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi),

@@ -280,7 +280,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       for (int j = 0; ok && j < n; ++j) {
         const int vi = 2 * j + 1, ki = 2 * j + 2;
         ok = landed(vi) && (j < n0 - 1 || wwait(&clean[j - (n0 - 1)], 0));
-        if (ok && j + 1 < n) ok = landed(ki);
         for (int t = 0; ok && t < 2; ++t) {
           const int nt = t ? n1 : n0;
           if (j >= nt) continue;
@@ -289,7 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           tc_fence_after();
           mma_values_half<D, 0>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi),
                                 idesc_v, j > 0);
-          ok = wwait(&p_late[t], j & 1);
+          // the next keys, while the second half's probabilities are formed
+          if (j + 1 < nt) ok = landed(ki);
+          ok = ok && wwait(&p_late[t], j & 1);
           if (!ok) break;
           tc_fence_after();
           mma_values_half<D, 1>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi),

@@ -9,11 +9,12 @@
 // in 32 bits with the rounding of rope_rotate_pair, rounded once to the type.
 // The matrix's transpose negates sin; a magnitude in the tables scales both.
 //
-// Bound by HBM: each value is read and written once, the tables' row once per
-// token. A block takes whole tokens, so a thread keeps its columns' cosines
-// and sines in registers over the heads that it turns.
-#include "serve_common.cuh"
-#include "rope_math.cuh"
+// Bound by HBM: each value is read and written once; the tables' row of a token
+// comes from L1 or L2 for all heads but the first. The position, then the
+// table's row, are two reads one after the other, so many warps are wanted; and
+// a thread keeps its columns' cosines and sines over its heads, as with one
+// head a thread the instructions were the bound.
+#include "rope_slots.cuh"
 
 namespace ajvp_serve {
 
@@ -32,67 +33,84 @@ struct RopeAtParams {
   int n_positions;
   int d, half;  // head dim, rot / 2
   int wide;     // positions are 64-bit
+  int parts;    // warps that share a token's heads
   float sign;   // +1, or -1 for the transpose
 };
 
-// Column groups of a head: a group is 8 adjacent columns (interleaved pairs,
-// or the columns behind the rotated part), or two times 8 columns half a
-// rotation apart.
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) rope_at_kernel(const __grid_constant__ RopeAtParams p) {
-  const int turned = HALF ? p.half / 8 : p.half / 4;  // groups with a rotation
-  const int groups = turned + (p.d - 2 * p.half) / 8;
-  const int lanes = kRopeThreads / groups;            // heads in flight
-  const int lane = threadIdx.x / groups, g = threadIdx.x - lane * groups;
-  if (lane >= lanes) return;
-  const int col = g < turned ? 8 * g : 2 * p.half + 8 * (g - turned);
-  const int heads = p.heads[0] + p.heads[1];
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-    const int64_t pos = p.wide ? static_cast<const int64_t*>(p.positions)[t]
-                               : static_cast<const int32_t*>(p.positions)[t];
-    if (pos < 0 || pos >= p.n_positions) {
-      if (threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
-      continue;
-    }
-    float c[8], s[8];
-    if (g < turned) {
-      const float* cp = p.cos + pos * p.half + (HALF ? col : col / 2);
-      const float* sp = p.sin + pos * p.half + (HALF ? col : col / 2);
+// A warp takes heads [n part / parts, n (part + 1) / parts) of q, then of k, of
+// one token: a lane takes a slot of 16 columns (rope_slots.cuh) of every
+// (32 / slots)-th head, two heads' loads in flight at a time. The first loads
+// go out before the position's and the table's, which wait for one another.
+template <typename T, int D, bool HALF>
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_at_kernel(const __grid_constant__ RopeAtParams p) {
+  constexpr int SLOTS = D / 16, STEP = 32 / SLOTS, U = 2;
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = int64_t(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = warp / p.parts;
+  if (t >= p.T) return;
+  const int part = static_cast<int>(warp - t * p.parts);
+  const RopeSlot sl(lane % SLOTS, p.half, HALF);
+  const int sub = lane / SLOTS;
+  const int64_t pos = p.wide ? static_cast<const int64_t*>(p.positions)[t]
+                             : static_cast<const int32_t*>(p.positions)[t];
+  float c[8], s[8];
+  bool ready = false, good = true;
 #pragma unroll
-      for (int i = 0; i < (HALF ? 8 : 4); i += 4) {
-        load4(cp + i, reinterpret_cast<float(&)[4]>(c[i]));
-        load4(sp + i, reinterpret_cast<float(&)[4]>(s[i]));
+  for (int w = 0; w < 2; ++w) {
+    const int hi = p.heads[w] * (part + 1) / p.parts;
+    int h = p.heads[w] * part / p.parts + sub;
+    const T* src = static_cast<const T*>(p.in[w]) + t * p.in_token[w] + h * p.in_head[w];
+    T* dst = static_cast<T*>(p.out[w]) + t * p.out_token[w] + h * p.out_head[w];
+    const int64_t in_step = STEP * p.in_head[w], out_step = STEP * p.out_head[w];
+    for (; h < hi; h += U * STEP) {
+      Raw8<T> ra[U], rb[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u * STEP < hi) {
+          ra[u].load(src + u * in_step + sl.c0);
+          rb[u].load(src + u * in_step + sl.c1);
+        }
+      if (!ready) {
+        ready = true;
+        good = pos >= 0 && pos < p.n_positions;
+        if (good && sl.pair >= 0) {
+          load_turn(p.cos, p.sin, pos, p.half, sl, c, s);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] *= p.sign;
+        }
       }
+      if (!good) break;
 #pragma unroll
-      for (int i = 0; i < (HALF ? 8 : 4); ++i) s[i] *= p.sign;
-    }
-    for (int h = lane; h < heads; h += lanes) {
-      const int w = h < p.heads[0] ? 0 : 1, hh = w ? h - p.heads[0] : h;
-      const T* src = static_cast<const T*>(p.in[w]) + t * p.in_token[w] + hh * p.in_head[w] + col;
-      T* dst = static_cast<T*>(p.out[w]) + t * p.out_token[w] + hh * p.out_head[w] + col;
-      float x[8];
-      load8(src, x);
-      if (HALF && g < turned) {
-        float y[8];
-        load8(src + p.half, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ajvp::rope_rotate_pair(x[i], y[i], c[i], s[i]);
-        store8(dst + p.half, y);
-      } else if (!HALF && g < turned) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ajvp::rope_rotate_pair(x[2 * i], x[2 * i + 1], c[i], s[i]);
-      }
-      store8(dst, x);
+      for (int u = 0; u < U; ++u)
+        if (h + u * STEP < hi) {
+          float a[8], b[8];
+          ra[u].unpack(a);
+          rb[u].unpack(b);
+          if (sl.pair >= 0) turn_slot(HALF, a, b, c, s);  // a rotated slot is split in the half layout
+          store8(dst + u * out_step + sl.c0, a);
+          store8(dst + u * out_step + sl.c1, b);
+        }
+      src += U * in_step;
+      dst += U * out_step;
     }
   }
+  if (!good && sub == 0) atomicOr(p.status, kStatusBadIndex);
 }
 
 template <typename T>
-void rope_at_launch(const RopeAtParams& p, int layout, int grid, cudaStream_t st) {
-  if (layout == ATTN_JVP_ROPE_HALF)
-    rope_at_kernel<T, true><<<grid, kRopeThreads, 0, st>>>(p);
+void rope_at_launch(RopeAtParams& p, bool half_layout, int sms, cudaStream_t st) {
+  // Warps of a token: one, so that the position and the table's row are read
+  // once, unless the tokens are too few to fill the SMs.
+  const int slots = p.d / 16, batch = 2 * (32 / slots);  // heads of about a round
+  const int rounds = (p.heads[0] + batch - 1) / batch;
+  const int64_t want = (int64_t(sms) * 32 + p.T - 1) / p.T;
+  p.parts = static_cast<int>(want < rounds ? want : rounds);
+  const int64_t warps = p.T * p.parts, per = kRopeThreads / 32;
+  const unsigned blocks = static_cast<unsigned>((warps + per - 1) / per);
+  if (p.d == 128)
+    (half_layout ? rope_at_kernel<T, 128, true> : rope_at_kernel<T, 128, false>)<<<blocks, kRopeThreads, 0, st>>>(p);
   else
-    rope_at_kernel<T, false><<<grid, kRopeThreads, 0, st>>>(p);
+    (half_layout ? rope_at_kernel<T, 64, true> : rope_at_kernel<T, 64, false>)<<<blocks, kRopeThreads, 0, st>>>(p);
 }
 
 }  // namespace ajvp_serve
@@ -108,7 +126,7 @@ extern "C" int attn_jvp_rope_at(const attn_jvp_tokens* shape, const void* q,
   const attn_jvp_tokens& s = *shape;
   const int bytes = dtype_bytes(s.dtype);
   if (!bytes || (s.d != 64 && s.d != 128)) return ATTN_JVP_ERR_UNSUPPORTED;
-  if (s.T < 0 || s.H < 1 || s.H > 65535 || (k && (s.Hkv < 1 || s.Hkv > 65535)) ||
+  if (s.T < 0 || s.T > (int64_t(1) << 31) - 1 || s.H < 1 || s.H > 65535 || (k && (s.Hkv < 1 || s.Hkv > 65535)) ||
       (k == nullptr) != (k_out == nullptr) || (position_bytes != 4 && position_bytes != 8))
     return ATTN_JVP_ERR_INVALID_ARGUMENT;
   int rc = check_tables(tables, s.d);
@@ -141,14 +159,12 @@ extern "C" int attn_jvp_rope_at(const attn_jvp_tokens* shape, const void* q,
   p.d = static_cast<int>(s.d);
   p.half = static_cast<int>(tables->rot / 2);
   p.sign = transpose ? -1.f : 1.f;
-  const int64_t cap = int64_t(sms) * 8;
-  const int grid = static_cast<int>(s.T < cap ? s.T : cap);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s.dtype == ATTN_JVP_BF16)
-    rope_at_launch<__nv_bfloat16>(p, tables->layout, grid, st);
+    rope_at_launch<__nv_bfloat16>(p, tables->layout == ATTN_JVP_ROPE_HALF, sms, st);
   else if (s.dtype == ATTN_JVP_F16)
-    rope_at_launch<__half>(p, tables->layout, grid, st);
+    rope_at_launch<__half>(p, tables->layout == ATTN_JVP_ROPE_HALF, sms, st);
   else
-    rope_at_launch<float>(p, tables->layout, grid, st);
+    rope_at_launch<float>(p, tables->layout == ATTN_JVP_ROPE_HALF, sms, st);
   return cudaGetLastError() == cudaSuccess ? ATTN_JVP_OK : ATTN_JVP_ERR_CUDA;
 }

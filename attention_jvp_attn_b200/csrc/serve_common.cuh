@@ -129,6 +129,27 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
     Elem<T>::unpack(u.w, x[6], x[7]);
   }
 }
+// The same eight elements as they lie in memory, and from there to 32 bits.
+template <typename T>
+struct Raw8 {
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void unpack(float (&x)[8]) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        x[2 * i] = __uint_as_float(w[2 * i]);
+        x[2 * i + 1] = __uint_as_float(w[2 * i + 1]);
+      } else {
+        Elem<T>::unpack(w[i], x[2 * i], x[2 * i + 1]);
+      }
+    }
+  }
+};
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   if constexpr (sizeof(T) == 4) {
