@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,27 +37,18 @@ class Mask(ctypes.Structure):
                 ("n_chunks", ctypes.c_int32)]
 
 
-class Tokens(ctypes.Structure):
-    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("Hkv", ctypes.c_int64),
-                ("d", ctypes.c_int64), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
-
-
 class Strides(ctypes.Structure):
     _fields_ = [("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
-class RopeTables(ctypes.Structure):
-    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
-                ("n_positions", ctypes.c_int64), ("rot", ctypes.c_int64),
-                ("layout", ctypes.c_int32)]
-
-
-class Cache(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64),
-                ("page_tokens", ctypes.c_int64), ("page_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
-                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
+# The other structs of the serving operators, as bytes (packing them costs a
+# fraction of what filling a ctypes.Structure does, and these calls are short):
+# shape (B, L, H, d, dtype, scale) and tokens (T, H, Hkv, d, dtype, scale),
+# rope_tables (cos, sin, n_positions, rot, layout), cache (k, v, k_scale,
+# v_scale, pages, page_tokens, three strides, two scale strides).
+pack_shape = pack_tokens = struct.Struct("@4qif").pack
+pack_rope_tables = struct.Struct("@QQqqi4x").pack
+pack_cache = struct.Struct("@4Q7q").pack
 
 
 MAX_GROUPS = 512
@@ -84,6 +76,8 @@ def load(path: str = None) -> ctypes.CDLL:
     """Load the in-tree CUDA library (or the library at `path`, e.g. the trace
     build, which then serves every later call); raise if it is missing."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -144,22 +138,20 @@ def load(path: str = None) -> ctypes.CDLL:
         lib.attn_jvp_debug_wait.argtypes = [ctypes.c_int64, ctypes.c_int32]
         lib.attn_jvp_debug_wait.restype = ctypes.c_int
         i64, i32 = ctypes.c_int64, ctypes.c_int32
-        lib.attn_jvp_rope_at.argtypes = [ctypes.POINTER(Tokens), vp, Strides, vp, Strides, vp, i32,
-                                         ctypes.POINTER(RopeTables), i32, vp, Strides, vp,
-                                         Strides, vp]
+        # vp where a struct or an array goes by pointer: bytes, or None
+        lib.attn_jvp_rope_at.argtypes = [vp, vp, Strides, vp, Strides, vp, i32, vp, i32, vp,
+                                         Strides, vp, Strides, vp]
         lib.attn_jvp_rope_at.restype = ctypes.c_int
-        lib.attn_jvp_cache_append.argtypes = [ctypes.POINTER(Tokens), vp, Strides, vp, Strides,
-                                              ctypes.POINTER(Cache), i64, vp, vp, vp, i64, i64,
-                                              ctypes.POINTER(RopeTables), vp]
+        lib.attn_jvp_cache_append.argtypes = [vp, vp, Strides, vp, Strides, vp, i64, vp, vp, vp,
+                                              i64, i64, vp, vp]
         lib.attn_jvp_cache_append.restype = ctypes.c_int
-        lib.attn_jvp_cache_attn.argtypes = [ctypes.POINTER(Shape), i64, vp, ctypes.POINTER(i64),
-                                            ctypes.POINTER(Cache), vp, vp, i64, i64, i64, i32, vp,
+        lib.attn_jvp_cache_attn.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp,
                                             i64, vp, vp, vp]
         lib.attn_jvp_cache_attn.restype = ctypes.c_int
-        lib.attn_jvp_cache_attn_workspace_bytes.argtypes = [ctypes.POINTER(Shape), i64, i64]
+        lib.attn_jvp_cache_attn_workspace_bytes.argtypes = [vp, i64, i64]
         lib.attn_jvp_cache_attn_workspace_bytes.restype = i64
-        lib.attn_jvp_prompt_attn.argtypes = [ctypes.POINTER(Tokens), vp, Strides, vp, Strides, vp,
-                                             Strides, i64, vp, vp, vp, vp]
+        lib.attn_jvp_prompt_attn.argtypes = [vp, vp, Strides, vp, Strides, vp, Strides, i64, vp,
+                                             vp, vp, vp]
         lib.attn_jvp_prompt_attn.restype = ctypes.c_int
         lib.attn_jvp_version.argtypes = []
         lib.attn_jvp_version.restype = ctypes.c_int32

@@ -24,9 +24,9 @@ device; one that is out of range is not used, and sync_status() then returns 7.
 """
 from __future__ import annotations
 
-import ctypes
 import functools
 import math
+import struct
 from typing import NamedTuple, Optional, Tuple
 
 import torch
@@ -36,6 +36,10 @@ from . import _abi
 _TYPES = {torch.bfloat16: _abi.DTYPE_BF16, torch.float32: _abi.DTYPE_F32,
           torch.float16: _abi.DTYPE_F16}
 _LAYOUTS = {"interleaved": _abi.ROPE_INTERLEAVED, "half": _abi.ROPE_HALF}
+_F8 = torch.float8_e4m3fn
+_pack3 = struct.Struct("@3q").pack
+# by value: the same numbers give the same (never changed) argument
+_strides = functools.lru_cache(maxsize=4096)(_abi.Strides)
 _NO_STRIDES = _abi.Strides(0, 0)
 
 
@@ -113,17 +117,18 @@ def rope_tables(rot: int, n_positions: int, base: float = 10000.0, scaling: Opti
 
 def _rows(t: torch.Tensor, what: str, like: Optional[torch.Tensor] = None) -> _abi.Strides:
     """Strides of a [T, heads, d] CUDA tensor whose d elements are adjacent."""
-    if t.dim() != 3:
+    st = t.stride()
+    if len(st) != 3:
         raise ValueError(f"{what} must be [T, heads, d]")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device or
-                             t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]):
-        raise ValueError(f"{what} must share tokens, head dim, dtype and device with the others")
-    st = t.stride()
+    if like is not None:
+        a, b = t.shape, like.shape
+        if a[0] != b[0] or a[2] != b[2] or t.dtype != like.dtype or t.device != like.device:
+            raise ValueError(f"{what} must share tokens, head dim, dtype and device with the others")
     if st[2] != 1:
         raise ValueError(f"the last dimension of {what} must be contiguous")
-    return _abi.Strides(st[0], st[1])
+    return _strides(st[0], st[1])
 
 
 def _int32(t: torch.Tensor, what: str, device: torch.device, *shape) -> int:
@@ -140,31 +145,30 @@ def _table(t: torch.Tensor, B: int, device: torch.device) -> int:
     return t.data_ptr()
 
 
-def _rope(cos: torch.Tensor, sin: torch.Tensor, layout: str, device: torch.device) -> _abi.RopeTables:
+def _rope(cos: torch.Tensor, sin: torch.Tensor, layout: str, device: torch.device) -> bytes:
     for t in (cos, sin):
         if t.dim() != 2 or t.shape != cos.shape or t.dtype != torch.float32 or \
                 t.device != device or not t.is_contiguous():
             raise ValueError("cos and sin must be contiguous fp32 [positions, rot/2] on the inputs' device")
     if layout not in _LAYOUTS:
         raise ValueError("layout is 'interleaved' or 'half'")
-    return _abi.RopeTables(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1],
-                           _LAYOUTS[layout])
+    n, half = cos.shape
+    return _abi.pack_rope_tables(cos.data_ptr(), sin.data_ptr(), n, 2 * half, _LAYOUTS[layout])
 
 
-def _cache(cache: PagedCache, device: torch.device) -> _abi.Cache:
+def _cache(cache: PagedCache, device: torch.device) -> bytes:
     k, v, ks, vs = cache
-    if k.dim() != 4 or k.dtype != torch.float8_e4m3fn or v.dtype != k.dtype or \
-            v.shape != k.shape or v.stride() != k.stride() or k.stride(3) != 1 or \
-            k.device != device or v.device != device:
+    st, ss = k.stride(), ks.stride()
+    if k.dim() != 4 or k.dtype != _F8 or v.dtype != _F8 or v.shape != k.shape or \
+            v.stride() != st or st[3] != 1 or k.device != device or v.device != device:
         raise ValueError("cache k and v must be float8_e4m3fn [pages, Hkv, page_tokens, d] of the "
                          "same strides, d contiguous, on the inputs' device")
     if ks.shape != k.shape[:2] or vs.shape != ks.shape or ks.dtype != torch.float32 or \
-            vs.dtype != torch.float32 or vs.stride() != ks.stride() or \
+            vs.dtype != torch.float32 or vs.stride() != ss or \
             ks.device != device or vs.device != device:
         raise ValueError("cache scales must be fp32 [pages, Hkv] of the same strides on the inputs' device")
-    st, ss = k.stride(), ks.stride()
-    return _abi.Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), k.shape[0],
-                      k.shape[2], st[0], st[1], st[2], ss[0], ss[1])
+    return _abi.pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), k.shape[0],
+                           k.shape[2], st[0], st[1], st[2], ss[0], ss[1])
 
 
 def _dtype(t: torch.Tensor, types=_TYPES) -> int:
@@ -176,13 +180,15 @@ def _dtype(t: torch.Tensor, types=_TYPES) -> int:
 
 def _call(fn, name: str, device: torch.device, *args) -> None:
     """fn(*args, stream) on the tensors' device and its current stream."""
-    stream = torch.cuda.current_stream(device).cuda_stream
+    # the stream's handle without an object around it: a few microseconds less
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if device.index == torch.cuda.current_device():
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
             rc = fn(*args, stream)
-    _abi.check(rc, name)
+    if rc != _abi.OK:
+        _abi.check(rc, name)
 
 
 def rope_at(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
@@ -203,18 +209,22 @@ def rope_at(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
     tables = _rope(cos, sin, layout, q.device)
     if out is None:
         qo = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-        ko = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k is not None else None
+        so = _strides(H * d, d)
+        ko, sko = None, _NO_STRIDES
+        if k is not None:
+            ko, sko = torch.empty(k.shape, dtype=q.dtype, device=q.device), _strides(k.shape[1] * d, d)
     else:
         qo, ko = out
         if qo.shape != q.shape or (k is None) != (ko is None) or \
                 (k is not None and ko.shape != k.shape):
             raise ValueError("out must give tensors of q's and k's shapes")
-    shape = _abi.Tokens(T, H, k.shape[1] if k is not None else 0, d, _dtype(q), 0.0)
-    _call(_abi.load().attn_jvp_rope_at, "attn_jvp_rope_at", q.device, ctypes.byref(shape),
-          q.data_ptr(), sq, k.data_ptr() if k is not None else None, sk, positions.data_ptr(),
-          positions.element_size(), ctypes.byref(tables), int(transpose), qo.data_ptr(),
-          _rows(qo, "out", q), ko.data_ptr() if ko is not None else None,
-          _rows(ko, "out", q) if ko is not None else _NO_STRIDES)
+        so = _rows(qo, "out", q)
+        sko = _rows(ko, "out", q) if ko is not None else _NO_STRIDES
+    shape = _abi.pack_tokens(T, H, k.shape[1] if k is not None else 0, d, _dtype(q), 0.0)
+    _call(_abi.load().attn_jvp_rope_at, "attn_jvp_rope_at", q.device, shape, q.data_ptr(), sq,
+          k.data_ptr() if k is not None else None, sk, positions.data_ptr(),
+          positions.element_size(), tables, int(transpose), qo.data_ptr(), so,
+          ko.data_ptr() if ko is not None else None, sko)
     return qo, ko
 
 
@@ -239,12 +249,12 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, starts: to
         raise ValueError("cos and sin go together")
     tables = _rope(cos, sin, layout, k.device) if cos is not None else None
     desc = _cache(cache, k.device)
-    shape = _abi.Tokens(T, heads, heads, d, _dtype(k), 0.0)
-    _call(_abi.load().attn_jvp_cache_append, "attn_jvp_cache_append", k.device,
-          ctypes.byref(shape), k.data_ptr(), sk, v.data_ptr(), sv, ctypes.byref(desc), B,
+    shape = _abi.pack_tokens(T, heads, heads, d, _dtype(k), 0.0)
+    _call(_abi.load().attn_jvp_cache_append, "attn_jvp_cache_append", k.device, shape,
+          k.data_ptr(), sk, v.data_ptr(), sv, desc, B,
           _int32(starts, "starts", k.device, B + 1), _int32(cached, "cached", k.device, B),
           _table(page_table, B, k.device), page_table.shape[1], page_table.stride(0),
-          ctypes.byref(tables) if tables is not None else None)
+          tables)
 
 
 _ATTN_TYPES = {torch.bfloat16: _abi.DTYPE_BF16, torch.float16: _abi.DTYPE_F16}
@@ -284,14 +294,14 @@ def cache_attn(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor,
     else:
         o, lse = out
         _check_out(o, lse, q, (B, n, H, d), (B, H, n))
-    shape = _abi.Shape(B, n, H, d, _dtype(q, _ATTN_TYPES), _scale(scale))
+    shape = _abi.pack_shape(B, n, H, d, _dtype(q, _ATTN_TYPES), _scale(scale))
     most = page_table.shape[1] * cache.k.shape[2]
     if 0 < max_len < most:
         most = max_len
     size = _workspace_bytes(q.device.index, n, H, d, Hkv, most)
     work = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
-    _call(_abi.load().attn_jvp_cache_attn, "attn_jvp_cache_attn", q.device, ctypes.byref(shape),
-          Hkv, q.data_ptr(), (ctypes.c_int64 * 3)(st[0], st[1], st[2]), ctypes.byref(desc),
+    _call(_abi.load().attn_jvp_cache_attn, "attn_jvp_cache_attn", q.device, shape, Hkv,
+          q.data_ptr(), _pack3(st[0], st[1], st[2]), desc,
           _int32(seq_lens, "seq_lens", q.device, B), _table(page_table, B, q.device),
           page_table.shape[1], page_table.stride(0), max_len, int(causal),
           work.data_ptr() if size else None, size, o.data_ptr(), lse.data_ptr())
@@ -302,7 +312,7 @@ def cache_attn(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor,
 def _workspace_bytes(device: int, n: int, H: int, d: int, Hkv: int, most: int) -> int:
     with torch.cuda.device(device):
         size = _abi.load().attn_jvp_cache_attn_workspace_bytes(
-            ctypes.byref(_abi.Shape(1, n, H, d, _abi.DTYPE_BF16, 0.0)), Hkv, most)
+            _abi.pack_shape(1, n, H, d, _abi.DTYPE_BF16, 0.0), Hkv, most)
     if size < 0:
         raise ValueError("bad shape, or no usable device")
     return size
@@ -336,8 +346,7 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch
     else:
         o, lse = out
         _check_out(o, lse, q, (T, H, d), (H, T))
-    shape = _abi.Tokens(T, H, k.shape[1], d, _dtype(q, _ATTN_TYPES), _scale(scale))
-    _call(_abi.load().attn_jvp_prompt_attn, "attn_jvp_prompt_attn", q.device, ctypes.byref(shape),
-          q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, B,
+    shape = _abi.pack_tokens(T, H, k.shape[1], d, _dtype(q, _ATTN_TYPES), _scale(scale))
+    _call(_abi.load().attn_jvp_prompt_attn, "attn_jvp_prompt_attn", q.device, shape, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, B,
           _int32(starts, "starts", q.device, B + 1), o.data_ptr(), lse.data_ptr())
     return o, lse
