@@ -85,58 +85,6 @@ __device__ __forceinline__ int reach_of(const CacheAttnParams& p, int b) {
   return checked_len(p, b);
 }
 
-// All steps, Hkv times those of each sequence, and the sequence that holds
-// step `w` with the number of steps before it. The whole block calls this.
-__device__ __forceinline__ void find_step(const CacheAttnParams& p, int64_t share, int64_t blocks,
-                                          int64_t& all, int& b, int64_t& before) {
-  __shared__ int64_t warp_sum[kRowsWarps];
-  __shared__ int64_t at[2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kThreads = kRowsWarps * 32;
-  auto own = [&](int i) -> int64_t { return i < p.B ? int64_t(p.Hkv) * steps_of(reach_of(p, i)) : 0; };
-  // inclusive sums of 128 sequences at a time
-  auto scan = [&](int64_t x, int64_t& total) -> int64_t {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    total = 0;
-    int64_t base = 0;
-#pragma unroll
-    for (int w = 0; w < kRowsWarps; ++w) {
-      if (w < warp) base += warp_sum[w];
-      total += warp_sum[w];
-    }
-    return base + x;
-  };
-  all = 0;
-  const int64_t first = own(threadIdx.x);  // kept for the second pass
-  for (int i0 = 0; i0 < p.B; i0 += kThreads) {
-    int64_t total;
-    scan(i0 == 0 ? first : own(i0 + threadIdx.x), total);
-    all += total;
-  }
-  const int64_t w = all * share / blocks;
-  int64_t passed = 0;
-  for (int i0 = 0; i0 < p.B; i0 += kThreads) {
-    const int64_t x = i0 == 0 ? first : own(i0 + threadIdx.x);
-    int64_t total;
-    const int64_t end = passed + scan(x, total);
-    if (w < end && w >= end - x) {
-      at[0] = i0 + threadIdx.x;
-      at[1] = end - x;
-    }
-    passed += total;
-  }
-  __syncthreads();
-  b = static_cast<int>(at[0]);
-  before = at[1];
-}
-
 // A lane's place in the instruction: g = lane / 4 its token (or column of O),
 // c = lane % 4 its columns (or tokens). Which tokens and which 16 codes those
 // stand for is free, and chosen so that the eight lanes of a shared-memory
@@ -168,17 +116,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) { return Elem<__half>::pack(a, b); }
-
-// What a block of the shared-out steps leaves for the join, behind all places
-// of the workspace.
-struct Piece {
-  static constexpr int kNone = -1, kEmpty = -2;
-  int went_on;  // b Hkv + hk of a tile that an earlier block began (in its first place), or
-                // kNone, or kEmpty for a block without steps
-  int begun;    // that of a tile that it began and a later block goes on with, or kNone
-  int place;    // where the begun tile's sums are
-  int unused;
-};
 
 // Four columns of row r of (b, hk) from its sums.
 template <typename T, int D>
@@ -230,7 +167,9 @@ __global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_k
   int64_t w = 0, w_end = 1, base = 0;  // base: the first step of (b, hk)
   if (params.work) {
     int64_t all;
-    find_step(p, blockIdx.x, gridDim.x, all, b, base);
+    find_step<kRowsWarps * 32>(
+        p.B, blockIdx.x, gridDim.x,
+        [&](int i) { return int64_t(p.Hkv) * steps_of(reach_of(p, i)); }, all, b, base);
     w = all * blockIdx.x / gridDim.x;
     w_end = all * (blockIdx.x + 1) / gridDim.x;
     const int steps = steps_of(reach_of(p, b));
@@ -705,27 +644,16 @@ __global__ void __launch_bounds__(kRowsWarps * 32) join_rows_kernel(const CacheA
   const int item = blockIdx.y * 32 + lane;
   const int r = item / (D / 4), col = (item % (D / 4)) * 4;
   const int rows = p.n * p.group;
-  float top = -INFINITY, sum = 0.f;
+  Join join;
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float mk, float lk, const float4& z) {
-    const float to = fmaxf(top, mk);
-    const float f = to == -INFINITY ? 1.f : ajvp::ex2_approx(top - to);
-    const float g = to == -INFINITY ? 1.f : ajvp::ex2_approx(mk - to);
-    sum = sum * f + lk * g;
-    y.x = y.x * f + z.x * g, y.y = y.y * f + z.y * g;
-    y.z = y.z * f + z.z * g, y.w = y.w * f + z.w * g;
-    top = to;
-  };
   if (warp == 0 && r < rows) {
     const float* at = work + (2 * int64_t(first) + pieces[first].place) * C::PLACE;
-    add(at[C::ROWS * D + r], at[C::ROWS * (D + 1) + r], *reinterpret_cast<const float4*>(at + r * D + col));
+    const float4 z = *reinterpret_cast<const float4*>(at + r * D + col);
+    join.add(at[C::ROWS * D + r], at[C::ROWS * (D + 1) + r], &y, &z, 1);
   }
-  // blocks first + 1 on, 32 at a time, until one that does not go on with the tile
-  for (int k0 = first + 1; k0 < blocks; k0 += 32) {
-    const int on = k0 + lane < blocks ? pieces[k0 + lane].went_on : -1;
-    const uint32_t ends = __ballot_sync(0xffffffffu, on != tile && on != Piece::kEmpty);
-    const uint32_t mine = __ballot_sync(0xffffffffu, on == tile);
-    const uint32_t use = ends ? mine & ((ends & -ends) - 1) : mine;
+  bool more = true;
+  for (int k0 = first + 1; more; k0 += 32) {
+    const uint32_t use = went_on(pieces, blocks, k0, tile, more);
     if (r < rows) {
       for (int i0 = warp; i0 < 32; i0 += 4 * kRowsWarps) {
         float mk[4], lk[4];
@@ -742,18 +670,17 @@ __global__ void __launch_bounds__(kRowsWarps * 32) join_rows_kernel(const CacheA
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) add(mk[i], lk[i], z[i]);
+        for (int i = 0; i < 4; ++i) join.add(mk[i], lk[i], &y, &z[i], 1);
       }
     }
-    if (ends) break;
   }
-  stats[0][warp][lane] = top, stats[1][warp][lane] = sum;
+  stats[0][warp][lane] = join.top, stats[1][warp][lane] = join.sum;
   part[warp][lane] = y;
   __syncthreads();
   if (warp == 0 && r < rows) {
 #pragma unroll
-    for (int w = 1; w < kRowsWarps; ++w) add(stats[0][w][lane], stats[1][w][lane], part[w][lane]);
-    write_row<T, D>(p, tile / p.Hkv, tile % p.Hkv, r, col, y, top, sum);
+    for (int w = 1; w < kRowsWarps; ++w) join.add(stats[0][w][lane], stats[1][w][lane], &y, &part[w][lane], 1);
+    write_row<T, D>(p, tile / p.Hkv, tile % p.Hkv, r, col, y, join.top, join.sum);
   }
 }
 
@@ -802,14 +729,25 @@ cudaError_t cache_rows_launch(const RowsParams& p, int d, int dtype, int blocks,
 // Blocks that share out the steps of long sequences: as many per SM as fit.
 constexpr int blocks_per_sm(int64_t rows) { return rows <= 8 ? 3 : 2; }
 
-// Whether sequences of up to `len` tokens are shared out over all blocks (a
-// second launch) rather than split within clusters.
-bool shared_out(int64_t rows, int64_t len) { return rows <= kRowsTile && len > 4096; }
-
-// Bytes of workspace per block: two places and what it leaves for the join.
-int64_t work_bytes(int64_t rows, int64_t d) {
-  return 2 * (rows <= 8 ? 8 : 16) * (d + 2) * 4 + static_cast<int64_t>(sizeof(Piece));
-}
+// How the work of a call with `rows` query rows per key head is shared out, for
+// sequences of up to `len` tokens: blocks (0: clusters, no workspace) and bytes
+// of workspace for each.
+struct Share {
+  int blocks;
+  int64_t bytes;
+  Share(int64_t rows, int64_t B, int64_t Hkv, int64_t d, int64_t len, int sms) : blocks(0), bytes(0) {
+    if (rows > kRowsTile) {
+      // tcgen05: a block per SM, but no more than give each four key tiles
+      const int64_t steps = B * Hkv * ((rows + kTilesRows - 1) / kTilesRows) * ((len + 127) / 128);
+      const int64_t most = (steps + 3) / 4;
+      blocks = static_cast<int>(most < sms ? most : sms);
+      bytes = tiles_work_bytes(d);
+    } else if (len > 4096) {
+      blocks = blocks_per_sm(rows) * sms;
+      bytes = 2 * (rows <= 8 ? 8 : 16) * (d + 2) * 4 + static_cast<int64_t>(sizeof(Piece));
+    }
+  }
+};
 
 }  // namespace
 
@@ -819,12 +757,11 @@ extern "C" int64_t attn_jvp_cache_attn_workspace_bytes(const attn_jvp_shape* sha
                                                        int64_t max_len) {
   using namespace ajvp_serve;
   if (!shape || Hkv < 1 || shape->H < 1 || shape->L < 0 || max_len < 0) return -1;
-  const int64_t rows = shape->L * (shape->H / Hkv);
-  if (!shared_out(rows, max_len)) return 0;
   unsigned int* status = nullptr;
   int sms = 0;
   if (ajvp::device_status_word(&status, &sms) != ATTN_JVP_OK) return -1;
-  return blocks_per_sm(rows) * int64_t(sms) * work_bytes(rows, shape->d);
+  const Share share(shape->L * (shape->H / Hkv), shape->B, Hkv, shape->d, max_len, sms);
+  return share.blocks * share.bytes;
 }
 
 extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, const void* q,
@@ -885,16 +822,14 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
   if (rows > (int64_t(1) << 30) || tiles > (int64_t(1) << 27)) return ATTN_JVP_ERR_UNSUPPORTED;
   p.row_tiles = static_cast<int>(row_tiles);
   p.splits = 1;
-  const bool share = shared_out(rows, len);
-  const int blocks = blocks_per_sm(rows) * sms;
-  if (share) {
-    if (!workspace || workspace_bytes < blocks * work_bytes(rows, s.d))
-      return ATTN_JVP_ERR_INVALID_ARGUMENT;
+  const Share share(rows, s.B, Hkv, s.d, len, sms);
+  if (share.blocks) {
+    if (!workspace || workspace_bytes < share.blocks * share.bytes) return ATTN_JVP_ERR_INVALID_ARGUMENT;
     if (!aligned16(workspace)) return ATTN_JVP_ERR_MISALIGNED;
-  }
-  rp.work = share ? static_cast<float*>(workspace) : nullptr;
-  if (few && !share)
+  } else {
     while (p.splits < 8 && tiles * p.splits < 2 * sms && len >= 256 * p.splits) p.splits *= 2;
+  }
+  rp.work = share.blocks ? static_cast<float*>(workspace) : nullptr;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (few) {
@@ -904,9 +839,9 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
         !ajvp::encode_cache_map(&rp.map_v, cache->v, s.d, cache->page_tokens, Hkv, cache->pages,
                                 p.token_stride, p.head_stride, p.page_stride, rp.box))
       return ATTN_JVP_ERR_INVALID_ARGUMENT;
-    e = cache_rows_launch(rp, static_cast<int>(s.d), s.dtype, blocks, st);
+    e = cache_rows_launch(rp, static_cast<int>(s.d), s.dtype, share.blocks, st);
   } else {
-    e = cache_tiles_launch(p, len, static_cast<int>(s.d), s.dtype, st);
+    e = cache_tiles_launch(p, static_cast<int>(s.d), s.dtype, share.blocks, rp.work, st);
   }
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? ATTN_JVP_OK : ATTN_JVP_ERR_CUDA;

@@ -42,7 +42,7 @@ __device__ __forceinline__ float read_scale(float s) {
 __device__ __forceinline__ int checked_len(const CacheAttnParams& p, int b) {
   const int len = p.lens[b];
   if (len >= 0 && len <= (int64_t(p.table_width) << p.page_shift)) return len;
-  if (threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+  atomicOr(p.status, kStatusBadIndex);
   return 0;
 }
 
@@ -83,10 +83,106 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   return v;
 }
 
+// What a block of the shared-out steps leaves for the join, behind all places
+// of the workspace (two places per block, for its first and its last piece).
+struct Piece {
+  static constexpr int kNone = -1, kEmpty = -2;
+  int went_on;  // number of a tile that an earlier block began (in its first place), or
+                // kNone, or kEmpty for a block without steps
+  int begun;    // that of a tile that it began and a later block goes on with, or kNone
+  int place;    // where the begun tile's sums are
+  int unused;
+};
+
+// The steps of all sequences in a row, own(b) of sequence b, are shared out to
+// `blocks` blocks: block k has steps [all k / blocks, all (k + 1) / blocks).
+// Gives `all`, the sequence that holds this block's first step, and the number
+// of steps before that sequence. The whole block calls this.
+template <int THREADS, typename Own>
+__device__ __forceinline__ void find_step(int B, int64_t share, int64_t blocks, Own own, int64_t& all,
+                                          int& b, int64_t& before) {
+  __shared__ int64_t warp_sum[THREADS / 32];
+  __shared__ int64_t at[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // inclusive sums over THREADS sequences at a time
+  auto scan = [&](int64_t x, int64_t& total) -> int64_t {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    total = 0;
+    int64_t base = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) base += warp_sum[w];
+      total += warp_sum[w];
+    }
+    return base + x;
+  };
+  all = 0;
+  const int64_t first = static_cast<int>(threadIdx.x) < B ? own(threadIdx.x) : 0;  // kept for the second pass
+  for (int i0 = 0; i0 < B; i0 += THREADS) {
+    const int i = i0 + threadIdx.x;
+    int64_t total;
+    scan(i0 == 0 ? first : i < B ? own(i) : 0, total);
+    all += total;
+  }
+  const int64_t w = all * share / blocks;
+  int64_t passed = 0;
+  for (int i0 = 0; i0 < B; i0 += THREADS) {
+    const int i = i0 + threadIdx.x;
+    const int64_t x = i0 == 0 ? first : i < B ? own(i) : 0;
+    int64_t total;
+    const int64_t end = passed + scan(x, total);
+    if (w < end && w >= end - x) {
+      at[0] = i;
+      at[1] = end - x;
+    }
+    passed += total;
+  }
+  __syncthreads();
+  b = static_cast<int>(at[0]);
+  before = at[1];
+}
+
+// Running join of pieces' sums of p v, maxima and sums of p.
+struct Join {
+  float top = -INFINITY, sum = 0.f;
+  __device__ __forceinline__ void add(float m, float l, float4* y, const float4* z, int n) {
+    const float to = fmaxf(top, m);
+    const float f = to == -INFINITY ? 1.f : ajvp::ex2_approx(top - to);
+    const float g = to == -INFINITY ? 1.f : ajvp::ex2_approx(m - to);
+    sum = sum * f + l * g;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      y[i].x = y[i].x * f + z[i].x * g, y[i].y = y[i].y * f + z[i].y * g;
+      y[i].z = y[i].z * f + z[i].z * g, y[i].w = y[i].w * f + z[i].w * g;
+    }
+    top = to;
+  }
+};
+
+// Blocks after `first`, in steps of 32 from k0 on, that went on with `tile`: a
+// bit each; `more` if the next 32 have to be looked at too. A whole warp.
+__device__ __forceinline__ uint32_t went_on(const Piece* pieces, int blocks, int k0, int tile, bool& more) {
+  const int k = k0 + static_cast<int>(threadIdx.x & 31);
+  const int on = k < blocks ? pieces[k].went_on : Piece::kNone;
+  const uint32_t ends = __ballot_sync(0xffffffffu, on != tile && on != Piece::kEmpty);
+  const uint32_t mine = __ballot_sync(0xffffffffu, on == tile);
+  more = ends == 0 && k0 + 32 < blocks;
+  return ends ? mine & ((ends & -ends) - 1) : mine;
+}
+
 constexpr int kRowsTile = 16;  // most query rows per key head of attn_cache_rows.cu
-// attn_cache_tiles.cu: pairs of tiles of 128 query rows on tcgen05, split for
-// sequences of up to `keys` tokens
-cudaError_t cache_tiles_launch(const CacheAttnParams& p, int64_t keys, int d, int dtype, cudaStream_t st);
+// attn_cache_tiles.cu: pairs of tiles of 128 query rows on tcgen05, on at most
+// tiles_blocks(sms) blocks; `work` has tiles_work_bytes of each.
+cudaError_t cache_tiles_launch(const CacheAttnParams& p, int d, int dtype, int blocks, float* work,
+                               cudaStream_t st);
+int64_t tiles_work_bytes(int64_t d);
 constexpr int kTilesRows = 256;
 
 }  // namespace ajvp_serve

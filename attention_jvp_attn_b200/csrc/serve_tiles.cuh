@@ -77,6 +77,13 @@ __device__ __forceinline__ void rescale_sums(uint32_t taddr, float f) {
   ajvp::tmem_wait_st();
 }
 
+// 64 scores of the lane's row.
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&s)[64]) {
+  ajvp::tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+  ajvp::tmem_ld32(taddr + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+  ajvp::tmem_wait_ld();
+}
+
 // Largest of 128 scores.
 __device__ __forceinline__ float max128(const uint32_t (&s)[kTile]) {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

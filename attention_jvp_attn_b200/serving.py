@@ -298,7 +298,7 @@ def cache_attn(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor,
     most = page_table.shape[1] * cache.k.shape[2]
     if 0 < max_len < most:
         most = max_len
-    size = _workspace_bytes(q.device.index, n, H, d, Hkv, most)
+    size = _workspace_bytes(q.device.index, B, n, H, d, Hkv, most)
     work = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
     _call(_abi.load().attn_jvp_cache_attn, "attn_jvp_cache_attn", q.device, shape, Hkv,
           q.data_ptr(), _pack3(st[0], st[1], st[2]), desc,
@@ -309,10 +309,10 @@ def cache_attn(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor,
 
 
 @functools.lru_cache(maxsize=1024)
-def _workspace_bytes(device: int, n: int, H: int, d: int, Hkv: int, most: int) -> int:
+def _workspace_bytes(device: int, B: int, n: int, H: int, d: int, Hkv: int, most: int) -> int:
     with torch.cuda.device(device):
         size = _abi.load().attn_jvp_cache_attn_workspace_bytes(
-            _abi.pack_shape(1, n, H, d, _abi.DTYPE_BF16, 0.0), Hkv, most)
+            _abi.pack_shape(B, n, H, d, _abi.DTYPE_BF16, 0.0), Hkv, most)
     if size < 0:
         raise ValueError("bad shape, or no usable device")
     return size
