@@ -71,26 +71,31 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
              : (((w & 0x7f807f80u) + 0x00800080u) >> 15) & 0x00010001u;
 }
 
-// The rank-th pair of row tiles of all sequences, those that see the most keys
-// first (so that the blocks started last are short, whatever the sequences'
-// order): its sequence b and its index k in it. Pairs of index k or above
-// number sum_b max(0, pairs(b) - k), so k is found by bisection and b among
-// the sequences that have a pair k. Every thread of the block calls this; false
-// if there are not so many pairs. The cost is one round of loads and log2 T /
-// 256 sums over the block.
+// The rank-th pair of row tiles of all sequences: its sequence b and its index
+// k in it. Up to kThreads sequences: those that see the most keys first, so
+// that the blocks started last are short whatever the sequences' order. Pairs
+// of index k or above number sum_b max(0, pairs(b) - k), so k is found by
+// bisection and b among the sequences that have a pair k: one round of loads
+// and log2 (T / 256) sums over the block. More sequences: in their order, by
+// find_sequence. Every thread of the block calls this; false if there is no
+// such pair.
 __device__ __forceinline__ bool find_pair(const PromptParams& p, int rank, int& b, int& k) {
   __shared__ int sums[kThreads / 32];
   __shared__ int found;
-  const int warp = threadIdx.x >> 5;
   auto pairs = [&](int i) -> int {
-    if (i >= p.B) return 0;
     const int raw0 = p.starts[i], raw1 = p.starts[i + 1];
     const int t0 = clamp_row(raw0, p.T), t1 = clamp_row(raw1, p.T);
     if (t0 != raw0 || t1 != raw1 || t1 < t0) atomicOr(p.status, kStatusBadIndex);
     return t1 > t0 ? (t1 - t0 + 2 * kTile - 1) / (2 * kTile) : 0;
   };
-  const int own = pairs(threadIdx.x);  // the first kThreads sequences stay in registers
-  auto total = [&](int x) -> int {     // over the block
+  if (p.B > kThreads) {
+    b = find_sequence(p.starts, p.B, p.T, 2 * kTile, 1, rank);
+    k = rank - (clamp_row(p.starts[b], p.T) / (2 * kTile) + b);
+    return k >= 0 && k < pairs(b);
+  }
+  const int warp = threadIdx.x >> 5;
+  const int own = static_cast<int>(threadIdx.x) < p.B ? pairs(threadIdx.x) : 0;
+  auto total = [&](int x) -> int {  // over the block
     x = __reduce_add_sync(0xffffffffu, x);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sums[warp] = x;
@@ -100,11 +105,7 @@ __device__ __forceinline__ bool find_pair(const PromptParams& p, int rank, int& 
     for (int w = 0; w < kThreads / 32; ++w) x += sums[w];
     return x;
   };
-  auto from = [&](int at) -> int {  // pairs of index `at` or above
-    int x = max(own - at, 0);
-    for (int i = threadIdx.x + kThreads; i < p.B; i += kThreads) x += max(pairs(i) - at, 0);
-    return total(x);
-  };
+  auto from = [&](int at) { return total(max(own - at, 0)); };  // pairs of index `at` or above
   int lo = 0, hi = p.T / (2 * kTile) + 1;  // from(lo) > rank >= from(hi)
   int above = 0;
   if (from(0) <= rank) return false;
@@ -118,24 +119,16 @@ __device__ __forceinline__ bool find_pair(const PromptParams& p, int rank, int& 
     }
   }
   k = lo;
-  int at = rank - above;  // among the sequences with a pair k
-  for (int i0 = 0; i0 < p.B; i0 += kThreads) {
-    const int i = i0 + threadIdx.x;
-    const bool has = (i0 == 0 ? own : pairs(i)) > k;
-    const uint32_t votes = __ballot_sync(0xffffffffu, has);
-    const int all = total((threadIdx.x & 31) == 0 ? __popc(votes) : 0);
-    if (at < all) {
-      int before = 0;
-      for (int w = 0; w < warp; ++w) before += sums[w];
-      before += __popc(votes & ((1u << (threadIdx.x & 31)) - 1u));
-      if (has && before == at) found = i;
-      __syncthreads();
-      b = found;
-      return true;
-    }
-    at -= all;
-  }
-  return false;
+  // the (rank - above)-th of the sequences with a pair k
+  const bool has = own > k;
+  const uint32_t votes = __ballot_sync(0xffffffffu, has);
+  total((threadIdx.x & 31) == 0 ? __popc(votes) : 0);
+  int before = __popc(votes & ((1u << (threadIdx.x & 31)) - 1u));
+  for (int w = 0; w < warp; ++w) before += sums[w];
+  if (has && before == rank - above) found = threadIdx.x;
+  __syncthreads();
+  b = found;
+  return true;
 }
 
 template <int D, bool F16>
@@ -163,8 +156,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int head = blockIdx.x % p.H;
-  int b, block;
-  if (!find_pair(p, static_cast<int>(blockIdx.x / p.H), b, block)) return;
+  __shared__ int where[2];
+  {
+    int b, block;
+    if (!find_pair(p, static_cast<int>(blockIdx.x / p.H), b, block)) return;
+    if (threadIdx.x == 0) where[0] = b, where[1] = block;
+    __syncthreads();
+  }
+  const int b = where[0], block = where[1];
   const int t0 = clamp_row(p.starts[b], p.T), t1 = clamp_row(p.starts[b + 1], p.T);
   const int first = block * 2 * kTile;  // the pair's first row
   const int len = t1 - t0;

@@ -198,19 +198,31 @@ __device__ __forceinline__ int clamp_row(int start, int T) { return min(max(star
 // first piece lies at least rows / unit + slack further, which is enough for
 // its rows however they straddle the pieces (slack = 1 for pieces that begin
 // with the sequence, 2 for pieces that may begin inside a page). So a block
-// finds its sequence by counting the first pieces at or before its own, in
-// one round of loads for up to blockDim.x sequences, and without any scan of
-// the lengths. Pieces that no sequence uses do nothing. Every thread of the
-// block calls this; the result is the same in all of them. It relies on
-// non-decreasing starts; others give some in-range sequence number.
+// finds its sequence without any scan of the lengths: by counting the first
+// pieces at or before its own, in one round of loads for up to blockDim.x
+// sequences, or by bisection if there are many more. Pieces that no sequence
+// uses do nothing. Every thread of the block calls this; the result is the same
+// in all of them. It relies on non-decreasing starts; others give some in-range
+// sequence number.
 __device__ __forceinline__ int find_sequence(const int32_t* starts, int B, int T, int unit,
                                              int slack, int piece) {
-  int before = 0;
-  for (int b0 = 0; b0 < B; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    const bool in =
-        b < B && clamp_row(starts[b], T) / unit + static_cast<int64_t>(slack) * b <= piece;
-    before += __syncthreads_count(in);
+  auto at_or_before = [&](int b) {
+    return clamp_row(starts[b], T) / unit + static_cast<int64_t>(slack) * b <= piece;
+  };
+  int before = 0;  // sequences whose first piece is at or before this one
+  if (B <= 4 * static_cast<int>(blockDim.x)) {
+    for (int b0 = 0; b0 < B; b0 += blockDim.x) {
+      const int b = b0 + threadIdx.x;
+      before += __syncthreads_count(b < B && at_or_before(b));
+    }
+  } else {
+    for (int lo = 0, hi = B; lo < hi;) {
+      const int mid = lo + (hi - lo) / 2;
+      if (at_or_before(mid))
+        before = lo = mid + 1;
+      else
+        hi = mid;
+    }
   }
   return before > 0 ? before - 1 : 0;
 }
