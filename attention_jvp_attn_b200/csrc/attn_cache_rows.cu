@@ -47,6 +47,7 @@ namespace {
 
 constexpr int kRowsWarps = 4;
 constexpr int kStep = 32;                  // tokens per step of a warp
+constexpr int kLeastSteps = 8;             // steps of a block: two of a warp
 constexpr uint32_t kHidden = 0xffffffffu;  // in place of a key scale: no page there
 
 struct RowsParams {
@@ -166,12 +167,16 @@ __global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_k
   int b, hk, rank = 0;
   int64_t w = 0, w_end = 1, base = 0;  // base: the first step of (b, hk)
   if (params.work) {
-    int64_t all;
+    int64_t all, blocks = gridDim.x;
     find_step<kRowsWarps * 32>(
-        p.B, blockIdx.x, gridDim.x,
-        [&](int i) { return int64_t(p.Hkv) * steps_of(reach_of(p, i)); }, all, b, base);
-    w = all * blockIdx.x / gridDim.x;
-    w_end = all * (blockIdx.x + 1) / gridDim.x;
+        p.B, blockIdx.x, kLeastSteps,
+        [&](int i) { return int64_t(p.Hkv) * steps_of(reach_of(p, i)); }, blocks, all, b, base);
+    if (blockIdx.x < blocks) {
+      w = all * blockIdx.x / blocks;
+      w_end = all * (blockIdx.x + 1) / blocks;
+    } else {
+      w = w_end = 0;
+    }
     const int steps = steps_of(reach_of(p, b));
     hk = static_cast<int>((w - base) / steps);
     base += int64_t(hk) * steps;
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_k
   float* scales = reinterpret_cast<float*>(smem + C::AT_SCALES + warp * C::SCALES);
   int issued = 0, taken = 0;  // steps whose copies were issued, and waited for
   bool first_piece = true;
-  Piece left = {w < w_end ? Piece::kNone : Piece::kEmpty, Piece::kNone, 0, 0};
+  Piece left = {Piece::kNone, Piece::kNone, 0, 0};
   while (w < w_end) {
     const int len = checked_len(p, b);
     const int reach = len;  // most keys seen
@@ -726,23 +731,35 @@ cudaError_t cache_rows_launch(const RowsParams& p, int d, int dtype, int blocks,
   return d == 128 ? rows_launch<__half, 128>(p, blocks, st) : rows_launch<__half, 64>(p, blocks, st);
 }
 
-// Blocks that share out the steps of long sequences: as many per SM as fit.
+// Blocks that share out the steps: as many per SM as fit (8 rows: 168 registers
+// and 70 KB; 16 rows: 255 and 104 KB. At 16 rows three blocks per SM spill and
+// took 231 us where two take 134).
 constexpr int blocks_per_sm(int64_t rows) { return rows <= 8 ? 3 : 2; }
 
 // How the work of a call with `rows` query rows per key head is shared out, for
 // sequences of up to `len` tokens: blocks (0: clusters, no workspace) and bytes
 // of workspace for each.
+//   - More than 16 rows go to the tcgen05 kernel: 8 sequences of 8,192 tokens, 8
+//     key heads, d = 128: 33 us at 4 rows and 45 us at 16 here, 88 us at 20 rows
+//     and 99 us at 128 there (two passes over 16 rows here would take 90 us).
+//   - Up to 16 rows, clusters (one launch) up to 512 tokens, or 4,096 if they are
+//     all resident at once; shared out evenly (two launches) beyond. us, clusters
+//     / shared out, single tokens, d = 128, by sequences x key heads and tokens:
+//       1 x 8:  512: 7.1 / 10.4   4,096: 11.5 / 12.1   16,384: 26.9 / 21.5
+//       16 x 2: 512: 7.5 / 10.7   4,096: 13.2 / 17.7   16,384: 32.4 / 34.8
+//       64 x 8: 512: 19.8 / 24.7  1,024: 36.7 / 35.1    8,192: 228 / 171
+//     and sequences of different lengths add to the second's advantage.
 struct Share {
   int blocks;
   int64_t bytes;
   Share(int64_t rows, int64_t B, int64_t Hkv, int64_t d, int64_t len, int sms) : blocks(0), bytes(0) {
     if (rows > kRowsTile) {
-      // tcgen05: a block per SM, but no more than give each four key tiles
+      // a block per SM, but no more than give each four key tiles
       const int64_t steps = B * Hkv * ((rows + kTilesRows - 1) / kTilesRows) * ((len + 127) / 128);
       const int64_t most = (steps + 3) / 4;
       blocks = static_cast<int>(most < sms ? most : sms);
       bytes = tiles_work_bytes(d);
-    } else if (len > 4096) {
+    } else if (len > 512 && (len > 4096 || B * Hkv * 8 > 2 * sms)) {
       blocks = blocks_per_sm(rows) * sms;
       bytes = 2 * (rows <= 8 ? 8 : 16) * (d + 2) * 4 + static_cast<int64_t>(sizeof(Piece));
     }

@@ -38,6 +38,7 @@ namespace {
 using namespace ajvp;
 
 constexpr int kTilesThreads = 512;
+constexpr int kLeastTiles = 2;    // key tiles of a block that takes part
 constexpr int kGroup = 16;        // tokens that share a page for certain
 constexpr int kScaleSlots = 8;    // key tiles whose scales are kept: more than the ring may run ahead
 
@@ -94,7 +95,7 @@ struct Current {
   int len, reach, first_edge, j_begin, n;
   int two, whole, valid;
 
-  __device__ void start(const CacheAttnParams& p, int64_t all, int b_, int64_t before, int blocks) {
+  __device__ void start(const CacheAttnParams& p, int64_t all, int b_, int64_t before, int64_t blocks) {
     index = done = twos = two_done = 0;
     w = all * blockIdx.x / blocks;
     w_end = all * (blockIdx.x + 1) / blocks;
@@ -295,14 +296,15 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
   __shared__ Current pc;
   __shared__ Piece left;  // what the join will know of this block
   {
-    int64_t all, before;
+    int64_t blocks = params.blocks, all, before;
     int b;
     find_step<kTilesThreads>(
-        p.B, blockIdx.x, params.blocks, [&](int i) { return p.Hkv * head_steps(p, checked_len(p, i)); },
-        all, b, before);
+        p.B, blockIdx.x, kLeastTiles, [&](int i) { return p.Hkv * head_steps(p, checked_len(p, i)); },
+        blocks, all, b, before);
     if (threadIdx.x == 0) {
-      pc.start(p, all, b, before, params.blocks);
-      left = {pc.valid ? Piece::kNone : Piece::kEmpty, Piece::kNone, 0, 0};
+      pc.valid = 0;
+      if (blockIdx.x < blocks) pc.start(p, all, b, before, blocks);
+      left = {Piece::kNone, Piece::kNone, 0, 0};
     }
     __syncthreads();
   }

@@ -86,21 +86,23 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 // What a block of the shared-out steps leaves for the join, behind all places
 // of the workspace (two places per block, for its first and its last piece).
 struct Piece {
-  static constexpr int kNone = -1, kEmpty = -2;
-  int went_on;  // number of a tile that an earlier block began (in its first place), or
-                // kNone, or kEmpty for a block without steps
+  static constexpr int kNone = -1;
+  int went_on;  // number of a tile that an earlier block began (in its first place), or kNone
   int begun;    // that of a tile that it began and a later block goes on with, or kNone
   int place;    // where the begun tile's sums are
   int unused;
 };
 
 // The steps of all sequences in a row, own(b) of sequence b, are shared out to
-// `blocks` blocks: block k has steps [all k / blocks, all (k + 1) / blocks).
-// Gives `all`, the sequence that holds this block's first step, and the number
-// of steps before that sequence. The whole block calls this.
+// `blocks` blocks: block k has steps [all k / blocks, all (k + 1) / blocks). Of
+// the blocks given only so many take part that each has `least` steps or more:
+// the lengths may be far below what the host could know. Gives `all`, the
+// blocks that take part, and for one of them the sequence that holds its first
+// step, and the number of steps before that sequence. The whole block calls
+// this.
 template <int THREADS, typename Own>
-__device__ __forceinline__ void find_step(int B, int64_t share, int64_t blocks, Own own, int64_t& all,
-                                          int& b, int64_t& before) {
+__device__ __forceinline__ void find_step(int B, int64_t share, int least, Own own, int64_t& blocks,
+                                          int64_t& all, int& b, int64_t& before) {
   __shared__ int64_t warp_sum[THREADS / 32];
   __shared__ int64_t at[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -131,7 +133,8 @@ __device__ __forceinline__ void find_step(int B, int64_t share, int64_t blocks, 
     scan(i0 == 0 ? first : i < B ? own(i) : 0, total);
     all += total;
   }
-  const int64_t w = all * share / blocks;
+  blocks = max(min(blocks, all / least), int64_t(1));
+  const int64_t w = all * min(share, blocks - 1) / blocks;
   int64_t passed = 0;
   for (int i0 = 0; i0 < B; i0 += THREADS) {
     const int i = i0 + threadIdx.x;
@@ -171,7 +174,7 @@ struct Join {
 __device__ __forceinline__ uint32_t went_on(const Piece* pieces, int blocks, int k0, int tile, bool& more) {
   const int k = k0 + static_cast<int>(threadIdx.x & 31);
   const int on = k < blocks ? pieces[k].went_on : Piece::kNone;
-  const uint32_t ends = __ballot_sync(0xffffffffu, on != tile && on != Piece::kEmpty);
+  const uint32_t ends = __ballot_sync(0xffffffffu, on != tile);
   const uint32_t mine = __ballot_sync(0xffffffffu, on == tile);
   more = ends == 0 && k0 + 32 < blocks;
   return ends ? mine & ((ends & -ends) - 1) : mine;
