@@ -144,8 +144,8 @@ struct Current {
 };
 
 // The address with bits of its offset flipped (the base is aligned beyond them).
-__device__ __forceinline__ const uint8_t* smem_xor(const uint8_t* p, uint32_t bits) {
-  return reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) ^ bits);
+__device__ __forceinline__ uint8_t* smem_xor(uint8_t* p, uint32_t bits) {
+  return reinterpret_cast<uint8_t*>(reinterpret_cast<uintptr_t>(p) ^ bits);
 }
 
 // What the softmax needs of the four groups of 64 scores.
@@ -482,7 +482,30 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
                                      scales[k * (kTile / kGroup) + lane % (kTile / kGroup)].y == -INFINITY);
         }
         if (!wwait(&raw_full[st], (run / stages) & 1)) break;
-        const uint8_t* from = stage_at(st) + from_at;
+        uint8_t* from = stage_at(st) + from_at;
+        const int left = reach - j * kTile;
+        const bool look = (i & 1) && j >= first_edge;
+        // Seldom, and so in the stage itself, a piece at a time (the lane's own):
+        // tokens that nobody sees, or without a page, become zeros; NaN values of
+        // tokens that some rows do not see too, and are marked.
+        if (left < kTile || hidden != 0 || look) {
+#pragma unroll 1
+          for (int k = 0; k < COUNT; ++k) {
+            const int block = (k / CH) * 4 + warp - 12, r = block * 8 + r7;
+            uint32_t* at = reinterpret_cast<uint32_t*>(
+                D == 128 ? smem_xor(from + block * 1024, (k % CH) << 6) : from + block * 512);
+            const bool none = r >= left || ((hidden >> (r / kGroup)) & 1u);
+            bool nan = false;
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t w = none ? 0u : at[e];
+              const uint32_t m = look ? (((w & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u : 0u;
+              nan |= m != 0;
+              at[e] = w & ~(m * 0xffu);
+            }
+            if (nan) atomicOr(&marked[4 * (j - first_edge) + (r >> 5)], 1u << (r & 31));
+          }
+        }
         // all pieces are read before the first is written: the compiler cannot
         // tell the two places apart
         uint4 u[COUNT];
@@ -495,30 +518,6 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
         }
         __syncwarp();
         mbar_arrive_if(&raw_empty[st], lane == 0);
-        // tokens that nobody sees, or without a page, become zeros
-        const int left = reach - j * kTile;
-        if (left < kTile || hidden != 0) {
-#pragma unroll
-          for (int k = 0; k < COUNT; ++k) {
-            const int r = ((k / CH) * 4 + warp - 12) * 8 + r7;
-            if (r >= left || ((hidden >> (r / kGroup)) & 1u)) u[k] = make_uint4(0, 0, 0, 0);
-          }
-        }
-        if ((i & 1) && j >= first_edge) {
-#pragma unroll
-          for (int k = 0; k < COUNT; ++k) {
-            const int r = ((k / CH) * 4 + warp - 12) * 8 + r7;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&u[k]);
-            bool nan = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t m = (((w[e] & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
-              nan |= m != 0;
-              w[e] &= ~(m * 0xffu);
-            }
-            if (nan) atomicOr(&marked[4 * (j - first_edge) + (r >> 5)], 1u << (r & 31));
-          }
-        }
         if (!wwait(&empty[slot], ((run / C::NS) & 1) ^ 1)) break;
         uint8_t* to = sRing + slot * C::TILE;
 #pragma unroll

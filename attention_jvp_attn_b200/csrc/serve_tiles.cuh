@@ -60,7 +60,7 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
 template <int D>
 __device__ __forceinline__ void rescale_sums(uint32_t taddr, float f) {
   const float2 f2 = make_float2(f, f);
-#pragma unroll
+#pragma unroll 1  // seldom run: small
   for (int x = 0; x < D; x += 32) {
     uint32_t r[32];
     ajvp::tmem_ld32(taddr + x, r);
