@@ -151,33 +151,34 @@ __device__ __forceinline__ uint8_t* smem_xor(uint8_t* p, uint32_t bits) {
 // What the softmax needs of the four groups of 64 scores.
 struct Groups {
   float a[4];    // score = a * product + lv, in powers of two with the value scale
-  float lv[4];   // log2 of the value scale; -inf for a group without a page
+  float lv[4];   // log2 of the value scale
   float inv[4];  // 1 / value scale
-  bool hidden;   // some group of the key tile has no page (the same for the whole block)
   __device__ __forceinline__ Groups(const float4* sc, float row_scale) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const float4 f = sc[g];
-      a[g] = row_scale * f.x, lv[g] = f.y, inv[g] = f.z;
-      hidden = f.w != 0.f;
+      // a group without a page has scores of -inf, and any finite addend will do
+      a[g] = row_scale * f.x, lv[g] = fmaxf(f.y, -64.f), inv[g] = f.z;
     }
   }
 };
 
-// Scores of tokens that the row does not see, from the left-th of 64 on or in
-// a group without a page, become -inf.
-__device__ __forceinline__ void hide(uint32_t (&s)[64], Groups& gr, int left) {
-  if (left >= 64 && !gr.hidden) return;
-  uint64_t seen = left >= 64 ? ~0ull : left <= 0 ? 0ull : (1ull << left) - 1;
+// Scores of tokens that the row does not see, from the left-th of 64 on or in a
+// group without a page, become -inf. In tensor memory, a group at a time:
+// seldom needed, so its code is kept small.
+__device__ __forceinline__ void hide(uint32_t taddr, const float4* sc, int left) {
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    const int here = sc[g].y == -INFINITY ? 0 : left - 16 * g;
+    uint32_t s[16];
+    ajvp::tmem_ld16(taddr + 16 * g, s);
+    ajvp::tmem_wait_ld();
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
-    if (gr.lv[g] == -INFINITY) {
-      gr.lv[g] = 0.f;  // any finite addend will do
-      seen &= ~(0xffffull << (16 * g));
-    }
-#pragma unroll
-  for (int x = 0; x < 64; ++x)
-    if (!((seen >> x) & 1)) s[x] = __float_as_uint(-INFINITY);
+    for (int x = 0; x < 16; ++x)
+      if (x >= here) s[x] = __float_as_uint(-INFINITY);
+    ajvp::tmem_st16(taddr + 16 * g, s);
+  }
+  ajvp::tmem_wait_st();
 }
 
 // Largest of 64 scores.
@@ -616,12 +617,12 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
         for (int h = 0; ok && h < 2; ++h) {
           uint32_t pk[32];
           float add;
+          if (j_begin + j >= first_edge || sc[0].w != 0.f) hide(tS + 64 * h, sc + 4 * h, left - 64 * h);
 #pragma unroll 1
           while (true) {
             uint32_t s[64];
             load_scores(tS + 64 * h, s);  // anew the second time: they need not be kept
-            Groups gr(sc + 4 * h, row_scale);
-            hide(s, gr, left - 64 * h);
+            const Groups gr(sc + 4 * h, row_scale);
             const float top = max_groups(s, gr);
             add = exp_groups(s, gr, m, pk);
             if (!__any_sync(0xffffffffu, top > m + kLazyMax)) break;
