@@ -20,6 +20,11 @@
 // same number of tiles, give or take one. Partial sums go to the workspace and
 // a second, small kernel joins them.
 //
+// Measured (one B200): 1,560 queries over 32,760 tokens, 12 heads, d = 128, 314
+// GFLOP: 412 us, 760 TFLOP/s. The bound is the chain scores -> softmax -> products
+// of a row tile, 4,100 to 4,600 cycles per key tile against 2,048 of tensor work;
+// the conversion is beside it (without it the time is the same).
+//
 // NaN values of tokens that some rows must not see are taken out of the
 // product and marked, as in attn_prompt.cu; a row that sees a marked token
 // gets NaN in its columns at the end.

@@ -19,7 +19,12 @@
 //     P_t are in tensor memory (128 columns each), the sums O_t beside them;
 //   - warps 10 and 11: look through the values of the tiles on the diagonal,
 //     whose keys some rows must not see (below).
-// Key tiles behind a row tile's last row are never visited.
+// Key tiles behind a row tile's last row are never visited. The first half of a
+// tile's probabilities is handed to the products before the second half is
+// formed. Measured (one B200, bf16): 32,760 tokens, 8 query and 2 key heads, d =
+// 128: 1.52 to 1.82 ms, 1,210 to 1,440 TFLOP/s by the power-capped clock; five
+// prompts of 61 to 8,192 tokens: 0.56 to 0.66 ms; 1,333 tokens, d = 64: 22.5 us. A
+// pair of key tiles takes 3,200 cycles, 2,048 of them tensor work.
 //
 // A masked key's probability is 0, but 0 times an infinity or NaN among its
 // values is not. So non-finite values in the tiles on the diagonal (which hold

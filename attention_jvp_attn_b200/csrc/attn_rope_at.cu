@@ -12,8 +12,11 @@
 // Bound by HBM: each value is read and written once; the tables' row of a token
 // comes from L1 or L2 for all heads but the first. The position, then the
 // table's row, are two reads one after the other, so many warps are wanted; and
-// a thread keeps its columns' cosines and sines over its heads, as with one
-// head a thread the instructions were the bound.
+// a thread keeps its columns' cosines and sines over its heads. Measured (one
+// B200): 32,760 tokens of 24 heads, d = 128, bf16, 419 MB: 77 us, 5.44 TB/s, 83 %
+// of the copy rate; with 8 columns of one head a thread 104 us (126 instructions
+// per 8 values), with a block per token that walks on to the next 107 us. 64
+// tokens of 40 heads: 3.1 us.
 #include "rope_slots.cuh"
 
 namespace ajvp_serve {
