@@ -15,7 +15,10 @@
 // reads and writes that page's codes and scale, so no atomics and no second
 // launch are needed. Each thread holds its values in registers between the
 // maximum and the rounding: one read of the input, one write of the codes.
-// Bound by HBM for prompts, by latency for single tokens.
+// Bound by instructions and latency for prompts (32,800 tokens in pages of 16, 8
+// heads, d = 128, 210 MB: 65 us, 3.2 TB/s, half of the copy rate; with one unit
+// per block and 8 columns a thread 129 us), by the five reads one after the other
+// for single tokens (64 sequences: 7.4 us).
 #include "rope_slots.cuh"
 
 namespace ajvp_serve {
@@ -209,7 +212,7 @@ extern "C" int attn_jvp_cache_append(const attn_jvp_tokens* shape, const void* k
   const attn_jvp_tokens& s = *shape;
   const int bytes = dtype_bytes(s.dtype);
   if (!bytes || (s.d != 64 && s.d != 128)) return ATTN_JVP_ERR_UNSUPPORTED;
-  if (s.T < 0 || s.T > (int64_t(1) << 30) || s.Hkv < 1 || s.Hkv > 65535 || B < 0 || B > (1 << 20))
+  if (s.T < 0 || s.T > (int64_t(1) << 30) || s.Hkv < 1 || s.Hkv > 32767 || B < 0 || B > (1 << 20))
     return ATTN_JVP_ERR_INVALID_ARGUMENT;
   int rc = check_cache(cache, s.Hkv, s.d);
   if (rc != ATTN_JVP_OK) return rc;

@@ -67,7 +67,7 @@ inline int check_cache(const attn_jvp_cache* c, int64_t Hkv, int64_t d) {
   if (c->page_stride % 16 || c->head_stride % 16 || c->token_stride % 16)
     return ATTN_JVP_ERR_MISALIGNED;
   if (c->page_stride >= int64_t(1) << 32 || c->token_stride >= int64_t(1) << 32)
-    return ATTN_JVP_ERR_UNSUPPORTED;  // page and row offsets are 32 x 32 -> 64 bit products
+    return ATTN_JVP_ERR_UNSUPPORTED;  // far below what tensor maps take (2^40)
   if (c->token_stride < d || (Hkv > 1 && c->head_stride < d) || (c->pages > 1 && c->page_stride < d) ||
       (c->pages > 1 && c->scale_page_stride < 1) || (Hkv > 1 && c->scale_head_stride < 1))
     return ATTN_JVP_ERR_INVALID_ARGUMENT;

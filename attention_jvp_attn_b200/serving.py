@@ -284,10 +284,11 @@ def cache_attn(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor,
     st = q.stride()
     if st[3] != 1:
         raise ValueError("the last dimension of q must be contiguous")
-    Hkv = cache.k.shape[1]
-    if cache.k.dim() != 4 or cache.k.shape[3] != d or H % Hkv:
+    Hkv = cache.k.shape[1] if cache.k.dim() == 4 else 0
+    if Hkv < 1 or cache.k.shape[3] != d or H % Hkv:
         raise ValueError("the cache must have q's head dim and a number of heads that divides q's")
     desc = _cache(cache, q.device)
+    lens_at, table_at = _int32(seq_lens, "seq_lens", q.device, B), _table(page_table, B, q.device)
     if out is None:
         o = torch.empty((B, n, H, d), dtype=q.dtype, device=q.device)
         lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
@@ -302,8 +303,7 @@ def cache_attn(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor,
     work = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
     _call(_abi.load().attn_jvp_cache_attn, "attn_jvp_cache_attn", q.device, shape, Hkv,
           q.data_ptr(), _pack3(st[0], st[1], st[2]), desc,
-          _int32(seq_lens, "seq_lens", q.device, B), _table(page_table, B, q.device),
-          page_table.shape[1], page_table.stride(0), max_len, int(causal),
+          lens_at, table_at, page_table.shape[1], page_table.stride(0), max_len, int(causal),
           work.data_ptr() if size else None, size, o.data_ptr(), lse.data_ptr())
     return o, lse
 
@@ -347,6 +347,7 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch
         o, lse = out
         _check_out(o, lse, q, (T, H, d), (H, T))
     shape = _abi.pack_tokens(T, H, k.shape[1], d, _dtype(q, _ATTN_TYPES), _scale(scale))
-    _call(_abi.load().attn_jvp_prompt_attn, "attn_jvp_prompt_attn", q.device, shape, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, B,
+    _call(_abi.load().attn_jvp_prompt_attn, "attn_jvp_prompt_attn", q.device, shape, q.data_ptr(),
+          sq, k.data_ptr(), sk, v.data_ptr(), sv, B,
           _int32(starts, "starts", q.device, B + 1), o.data_ptr(), lse.data_ptr())
     return o, lse

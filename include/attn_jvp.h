@@ -485,6 +485,7 @@ int32_t attn_jvp_version(void);
  * its outputs: by default they are left as they were), and
  * attn_jvp_sync_status reports ATTN_JVP_ERR_BAD_INDEX later.
  *
+ * Outputs do not overlap inputs unless the function says that they may.
  * No function here synchronizes, allocates device memory or keeps state
  * between calls, so each can be captured in a CUDA graph, and calls on
  * several streams may overlap as long as their outputs do not.
@@ -554,7 +555,7 @@ typedef struct {
   float* v_scale;
   int64_t pages;       /* pages in the pool, >= 1 */
   int64_t page_tokens; /* 16, 32, 64 or 128 */
-  int64_t page_stride, head_stride, token_stride;     /* of k and v; multiples of 16 */
+  int64_t page_stride, head_stride, token_stride;  /* of k and v; multiples of 16; the first and last below 2^32 */
   int64_t scale_page_stride, scale_head_stride;       /* of k_scale and v_scale */
 } attn_jvp_cache;
 
@@ -574,7 +575,8 @@ typedef struct {
  * Rows of a page behind the last appended token are left as they were. Calling
  * it twice with the same arguments gives the same cache.
  *
- *   shape    T = tokens in k and v; Hkv, d, dtype (all three types)
+ *   shape    T = tokens in k and v, <= 2^30; Hkv <= 32767, d, dtype (all three types);
+ *            B <= 2^20
  *   starts   [B + 1] int32, non-decreasing, starts[0] >= 0, starts[B] <= T;
  *            rows outside them are ignored
  *   cached   [B] int32, tokens of each sequence in the cache before the call
@@ -596,7 +598,7 @@ int attn_jvp_cache_append(const attn_jvp_tokens* shape, const void* k, attn_jvp_
  * i of n (causal != 0: the n queries are the sequence's last n tokens). A row
  * that sees no key gets O = 0, LSE = -infinity.
  *
- *   shape   B = sequences, L = n, H, d, dtype (bf16 or fp16), scale
+ *   shape   B = sequences <= 65535, L = n <= 2^24, H, d, dtype (bf16 or fp16), scale
  *   Hkv     key/value heads
  *   q       [B, n, H, d]: q_strides[0..2] in elements for B, n, H
  *   lens    [B] int32, tokens of each sequence in the cache, the new ones
@@ -635,7 +637,7 @@ int64_t attn_jvp_cache_attn_workspace_bytes(const attn_jvp_shape* shape, int64_t
  * they were.
  *
  *   shape   T, H, Hkv, d, dtype (bf16 or fp16), scale
- *   starts  [B + 1] int32, as for attn_jvp_cache_append
+ *   starts  [B + 1] int32, as for attn_jvp_cache_append; B <= 2^20
  *   o       [T, H, d] dense, of dtype;  lse [H, T] float dense
  */
 int attn_jvp_prompt_attn(const attn_jvp_tokens* shape, const void* q, attn_jvp_strides q_strides,

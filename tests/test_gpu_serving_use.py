@@ -267,6 +267,67 @@ def test_empty_calls():
     assert same(before, cache.k)
 
 
+# ------------------------------------------------------------------ refusals
+def test_wrong_arguments_are_refused():
+    """Calls that need tensors on the GPU to be refused; nothing is launched."""
+    g = rng(8)
+    cache = filled(g, 4, 2, 16, 64)
+    q, lens, table = randn(g, 2, 1, 4, 64), ints([5, 6]), ints([[0], [1]])
+    flat = aj.PagedCache(cache.k[0], cache.v[0], cache.k_scale, cache.v_scale)
+    for bad in (dict(q=q[0]), dict(q=q.float()), dict(q=randn(g, 2, 1, 3, 64)), dict(q=randn(g, 2, 1, 4, 128)),
+                dict(q=q.transpose(2, 3)), dict(cache=flat), dict(cache=cache._replace(k_scale=cache.k_scale[:3])),
+                dict(cache=cache._replace(v=cache.v.view(torch.uint8))), dict(seq_lens=lens.long()),
+                dict(seq_lens=lens[:1]), dict(seq_lens=lens.cpu()), dict(page_table=table[:, 0]),
+                dict(page_table=table[:1]), dict(page_table=table.long()), dict(scale=-1.0), dict(max_len=-1),
+                dict(out=(q, torch.empty(2, 4, 2, device="cuda")))):
+        args = dict(q=q, cache=cache, seq_lens=lens, page_table=table) | bad
+        with pytest.raises((ValueError, TypeError, RuntimeError)):
+            aj.cache_attn(**args)
+    k, starts, cached = randn(g, 3, 2, 64), ints([0, 1, 3]), ints([2, 2])
+    for bad in (dict(cache=flat), dict(k=k[:, :1]), dict(v=k[:2]), dict(starts=starts[:2]), dict(cached=cached[:1]),
+                dict(page_table=table[0]), dict(cos=torch.ones(9, 32, device="cuda")), dict(layout="other", cos=1, sin=1)):
+        args = dict(cache=cache, k=k, v=k, starts=starts, cached=cached, page_table=table) | bad
+        with pytest.raises((ValueError, AttributeError)):
+            aj.cache_append(**args)
+    with pytest.raises(ValueError):
+        aj.prompt_attn(k[:, :1], k, k, starts)
+    ok()
+
+
+@pytest.mark.parametrize("n,pages", [(1, 400), (20, 4)])
+def test_workspace_is_checked(n, pages):
+    """The C entry with the workspace that it asks for, with less, and with none."""
+    from attention_jvp_attn_b200 import _abi
+    lib = _abi.load()
+    g = rng(8)
+    cache = filled(g, pages, 1, 16, 64)
+    q = randn(g, 1, n, 1, 64)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    lens = ints([16 * pages])
+    want, _ = aj.cache_attn(q, cache, lens, table)
+    o, lse = torch.full_like(want, 3.0), torch.empty(1, 1, n, device="cuda")
+    shape = _abi.pack_shape(1, n, 1, 64, _abi.DTYPE_BF16, 0.0)
+    size = lib.attn_jvp_cache_attn_workspace_bytes(shape, 1, 16 * pages)
+    assert size > 0
+    work = torch.empty(size + 16, dtype=torch.uint8, device="cuda")
+
+    def call(at, bytes_):
+        import ctypes
+        desc = _abi.pack_cache(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
+                               pages, 16, *cache.k.stride()[:3], *cache.k_scale.stride())
+        rc = lib.attn_jvp_cache_attn(shape, 1, q.data_ptr(), (ctypes.c_int64 * 3)(*q.stride()[:3]), desc,
+                                     lens.data_ptr(), table.data_ptr(), pages, pages, 0, 1, at, bytes_,
+                                     o.data_ptr(), lse.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        ok()
+        return rc
+
+    assert call(None, 0) == call(work.data_ptr(), size - 1) == call(None, size) == _abi.ERR_INVALID_ARGUMENT
+    assert call(work.data_ptr() + 8, size) == _abi.ERR_MISALIGNED
+    assert (o == 3).all()
+    assert call(work.data_ptr(), size) == _abi.OK
+    assert torch.equal(o, want)
+
+
 # ------------------------------------------------------------------ many sequences
 def test_many_sequences():
     """More sequences than a block has threads: empty, single and two-tile ones."""

@@ -81,7 +81,8 @@ def append(lib, T=8, Hkv=2, d=64, dtype=BF16, k=P[6], sk=(128, 64), v=P[7], sv=(
     (dict(c=cache(pages=0)), INVALID), (dict(c=cache(page=48)), UNSUPPORTED), (dict(c=cache(page=256)), UNSUPPORTED),
     (dict(c=cache(strides=(8192, 4096, 72))), MISALIGNED), (dict(c=cache(strides=(8192, 4096, 48))), INVALID),
     (dict(c=cache(strides=(8192, 32, 64))), INVALID), (dict(c=cache(strides=(2 ** 32, 4096, 64))), UNSUPPORTED),
-    (dict(c=cache(scale=(0, 1))), INVALID), (dict(c=cache(scale=(2, 0))), INVALID)])
+    (dict(c=cache(scale=(0, 1))), INVALID), (dict(c=cache(scale=(2, 0))), INVALID), (dict(Hkv=32768), INVALID),
+    (dict(width=2 ** 62, stride=2 ** 62), INVALID), (dict(T=2 ** 31), INVALID), (dict(B=2 ** 21), INVALID)])
 def test_cache_append_refuses(lib, bad, code):
     assert append(lib, **bad) == code
 
@@ -101,7 +102,8 @@ def attn(lib, B=2, n=1, H=4, Hkv=2, d=64, dtype=BF16, scale=0.0, q=P[6], sq=(256
     (dict(sq=(260, 256, 64)), MISALIGNED), (dict(sq=(256, 256, -64)), INVALID), (dict(lens=None), INVALID),
     (dict(table=None), INVALID), (dict(o=None), INVALID), (dict(o=P[9] + 8), MISALIGNED), (dict(lse=None), INVALID),
     (dict(width=0), INVALID), (dict(width=2 ** 25), INVALID), (dict(max_len=-1), INVALID), (dict(c=cache(page=8)), UNSUPPORTED),
-    (dict(B=65536), INVALID)])
+    (dict(B=65536), INVALID), (dict(width=2 ** 60, stride=2 ** 60), INVALID), (dict(n=2 ** 25), INVALID),
+    (dict(H=65536), INVALID), (dict(c=cache(strides=(8192, 4096, 2 ** 32))), UNSUPPORTED)])
 def test_cache_attn_refuses(lib, bad, code):
     assert attn(lib, **bad) == code
 
@@ -120,6 +122,14 @@ def prompt(lib, T=8, H=4, Hkv=2, d=64, dtype=BF16, scale=0.0, q=P[0], sq=(512, 6
     (dict(starts=None), INVALID), (dict(o=None), INVALID), (dict(o=P[4] + 8), MISALIGNED), (dict(lse=None), INVALID)])
 def test_prompt_attn_refuses(lib, bad, code):
     assert prompt(lib, **bad) == code
+
+
+@pytest.mark.parametrize("bad", [dict(B=-1), dict(n=-1), dict(n=2 ** 62), dict(H=3), dict(H=0), dict(Hkv=0), dict(d=96),
+                                 dict(dtype=F32), dict(max_len=-1), dict(max_len=2 ** 62)])
+def test_workspace_bytes_refuses(lib, bad):
+    a = dict(B=2, n=1, H=4, Hkv=2, d=64, dtype=BF16, max_len=5000) | bad
+    shape = _abi.pack_shape(a["B"], a["n"], a["H"], a["d"], a["dtype"], 0.0)
+    assert lib.attn_jvp_cache_attn_workspace_bytes(shape, a["Hkv"], a["max_len"]) == -1
 
 
 def test_fp16_is_refused_elsewhere(lib):
