@@ -76,11 +76,13 @@ def load_peaks():
 
 
 def kernel_source_hash() -> str:
-    """Hash of the sources the forward kernels are built from (the backward's
-    and the rotary embedding's own source files do not change them)."""
+    """Hash of the sources the forward kernels are built from (the backward's, the
+    rotary embedding's and the serving operators' own source files do not change
+    them)."""
     h = hashlib.sha256()
     for p in sorted(glob.glob(os.path.join(ROOT, "attention_jvp_attn_b200", "csrc", "*"))):
-        if os.path.basename(p).startswith(("attn_jvp_bwd", "attn_jvp_rope")):
+        if os.path.basename(p).startswith(("attn_jvp_bwd", "attn_jvp_rope", "attn_cache", "attn_prompt",
+                                           "attn_rope_at", "rope_slots", "serve_")):
             continue
         with open(p, "rb") as f:
             h.update(os.path.basename(p).encode())
