@@ -221,6 +221,7 @@ extern "C" int attn_jvp_cache_append(const attn_jvp_tokens* shape, const void* k
     return ATTN_JVP_ERR_INVALID_ARGUMENT;
   if (s.T == 0 || B == 0) return ATTN_JVP_OK;
   if (!starts || !cached || !table) return ATTN_JVP_ERR_INVALID_ARGUMENT;
+  if (!aligned4(starts) || !aligned4(cached) || !aligned4(table)) return ATTN_JVP_ERR_MISALIGNED;
   if ((rc = check_rows(k, k_strides, s.T, s.Hkv, bytes)) != ATTN_JVP_OK ||
       (rc = check_rows(v, v_strides, s.T, s.Hkv, bytes)) != ATTN_JVP_OK)
     return rc;

@@ -811,7 +811,8 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
     return ATTN_JVP_ERR_INVALID_ARGUMENT;
   if (s.B == 0 || s.L == 0) return ATTN_JVP_OK;
   if (!q || !lens || !table || !o || !lse) return ATTN_JVP_ERR_INVALID_ARGUMENT;
-  if (!aligned16(q) || !aligned16(o) || (s.B > 1 && q_strides[0] % 8) ||
+  if (!aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(lens) || !aligned4(table) ||
+      (s.B > 1 && q_strides[0] % 8) ||
       (s.L > 1 && q_strides[1] % 8) || (s.H > 1 && q_strides[2] % 8))
     return ATTN_JVP_ERR_MISALIGNED;
   if ((s.B > 1 && q_strides[0] < 0) || (s.L > 1 && q_strides[1] < 0) || (s.H > 1 && q_strides[2] < 0))

@@ -482,11 +482,11 @@ extern "C" int attn_jvp_prompt_attn(const attn_jvp_tokens* shape, const void* q,
     return ATTN_JVP_ERR_INVALID_ARGUMENT;
   if (s.T == 0 || B == 0) return ATTN_JVP_OK;
   if (!starts || !o || !lse) return ATTN_JVP_ERR_INVALID_ARGUMENT;
-  if (!aligned16(o)) return ATTN_JVP_ERR_MISALIGNED;
+  if (!aligned16(o) || !aligned4(lse) || !aligned4(starts)) return ATTN_JVP_ERR_MISALIGNED;
   int rc;
-  if ((rc = check_rows(q, q_strides, s.T, s.H, 2)) != ATTN_JVP_OK ||
-      (rc = check_rows(k, k_strides, s.T, s.Hkv, 2)) != ATTN_JVP_OK ||
-      (rc = check_rows(v, v_strides, s.T, s.Hkv, 2)) != ATTN_JVP_OK)
+  if ((rc = check_rows_map(q, q_strides, s.T, s.H, s.d, 2)) != ATTN_JVP_OK ||
+      (rc = check_rows_map(k, k_strides, s.T, s.Hkv, s.d, 2)) != ATTN_JVP_OK ||
+      (rc = check_rows_map(v, v_strides, s.T, s.Hkv, s.d, 2)) != ATTN_JVP_OK)
     return rc;
   const int64_t pieces = s.T / (2 * kTile) + B;
   if (pieces * s.H > (int64_t(1) << 30)) return ATTN_JVP_ERR_UNSUPPORTED;

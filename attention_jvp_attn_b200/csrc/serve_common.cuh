@@ -22,6 +22,8 @@ constexpr uint32_t kStatusBadIndex = 2u;  // bit of the device status word
 // ---- host: argument checks ----
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 inline int dtype_bytes(int32_t dtype) {
   return dtype == ATTN_JVP_F32 ? 4 : (dtype == ATTN_JVP_BF16 || dtype == ATTN_JVP_F16) ? 2 : 0;
 }
@@ -35,6 +37,15 @@ inline int check_rows(const void* p, attn_jvp_strides s, int64_t rows, int64_t h
       (heads > 1 && (s.head < 0 || s.head * bytes % 16)))
     return ATTN_JVP_ERR_MISALIGNED;
   return ATTN_JVP_OK;
+}
+
+// The same for an input that tensor maps read: rows and heads may not be one
+// and the same (a stride of 0).
+inline int check_rows_map(const void* p, attn_jvp_strides s, int64_t rows, int64_t heads, int64_t d,
+                          int bytes) {
+  const int rc = check_rows(p, s, rows, heads, bytes);
+  if (rc != ATTN_JVP_OK) return rc;
+  return (rows > 1 && s.token < d) || (heads > 1 && s.head < d) ? ATTN_JVP_ERR_INVALID_ARGUMENT : ATTN_JVP_OK;
 }
 
 // The same for an output: rows and heads must not fall on one another.
@@ -63,7 +74,8 @@ inline int check_cache(const attn_jvp_cache* c, int64_t Hkv, int64_t d) {
   if (c->pages < 1 || c->pages > (int64_t(1) << 31) - 1) return ATTN_JVP_ERR_INVALID_ARGUMENT;
   if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128)
     return ATTN_JVP_ERR_UNSUPPORTED;
-  if (!aligned16(c->k) || !aligned16(c->v)) return ATTN_JVP_ERR_MISALIGNED;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale))
+    return ATTN_JVP_ERR_MISALIGNED;
   if (c->page_stride % 16 || c->head_stride % 16 || c->token_stride % 16)
     return ATTN_JVP_ERR_MISALIGNED;
   if (c->page_stride >= int64_t(1) << 32 || c->token_stride >= int64_t(1) << 32)

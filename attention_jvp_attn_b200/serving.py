@@ -140,7 +140,7 @@ def _int32(t: torch.Tensor, what: str, device: torch.device, *shape) -> int:
 
 def _table(t: torch.Tensor, B: int, device: torch.device) -> int:
     if t.dim() != 2 or t.dtype != torch.int32 or t.device != device or t.shape[0] != B or \
-            t.shape[1] < 1 or t.stride(1) != 1:
+            t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("page_table must be int32 [B, pages] with contiguous rows on the inputs' device")
     return t.data_ptr()
 

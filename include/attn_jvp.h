@@ -475,8 +475,9 @@ int32_t attn_jvp_version(void);
  *
  * Token rows are [T, heads, d] arrays with a stride per token and per head
  * (in elements; the d elements of a head are adjacent), so views of a fused
- * projection can be passed. Every pointer is 16-byte aligned and every
- * stride a multiple of 16 bytes. Query heads are grouped: query head h reads
+ * projection can be passed. Rows, codes and rotation tables are 16-byte
+ * aligned, with strides of whole 16 bytes; integers, scales and lse as their
+ * type is. Query heads are grouped: query head h reads
  * key head h / (H / Hkv); H is a multiple of Hkv.
  *
  * Positions, lengths and page numbers are device data, which the host cannot
@@ -637,6 +638,8 @@ int64_t attn_jvp_cache_attn_workspace_bytes(const attn_jvp_shape* shape, int64_t
  * they were.
  *
  *   shape   T, H, Hkv, d, dtype (bf16 or fp16), scale
+ *   q, k, v  with strides of at least d (of 0 nowhere: give Hkv the number of
+ *           key heads that there are)
  *   starts  [B + 1] int32, as for attn_jvp_cache_append; B <= 2^20
  *   o       [T, H, d] dense, of dtype;  lse [H, T] float dense
  */

@@ -291,6 +291,11 @@ def test_wrong_arguments_are_refused():
             aj.cache_append(**args)
     with pytest.raises(ValueError):
         aj.prompt_attn(k[:, :1], k, k, starts)
+    with pytest.raises(RuntimeError):  # one key head for two, by a stride of 0
+        aj.prompt_attn(k, k[:, :1].expand(3, 2, 64), k, starts)
+    ok()
+    one = ints([0, 1])[:, None]  # a column whose own stride means nothing
+    assert torch.equal(aj.cache_attn(q, cache, lens, table)[0], aj.cache_attn(q, cache, lens, one)[0])
     ok()
 
 

@@ -82,7 +82,9 @@ def append(lib, T=8, Hkv=2, d=64, dtype=BF16, k=P[6], sk=(128, 64), v=P[7], sv=(
     (dict(c=cache(strides=(8192, 4096, 72))), MISALIGNED), (dict(c=cache(strides=(8192, 4096, 48))), INVALID),
     (dict(c=cache(strides=(8192, 32, 64))), INVALID), (dict(c=cache(strides=(2 ** 32, 4096, 64))), UNSUPPORTED),
     (dict(c=cache(scale=(0, 1))), INVALID), (dict(c=cache(scale=(2, 0))), INVALID), (dict(Hkv=32768), INVALID),
-    (dict(width=2 ** 62, stride=2 ** 62), INVALID), (dict(T=2 ** 31), INVALID), (dict(B=2 ** 21), INVALID)])
+    (dict(width=2 ** 62, stride=2 ** 62), INVALID), (dict(T=2 ** 31), INVALID), (dict(B=2 ** 21), INVALID),
+    (dict(starts=P[8] + 2), MISALIGNED), (dict(cached=P[9] + 1), MISALIGNED), (dict(table=P[10] + 2), MISALIGNED),
+    (dict(c=cache(ks=P[4] + 2)), MISALIGNED)])
 def test_cache_append_refuses(lib, bad, code):
     assert append(lib, **bad) == code
 
@@ -103,7 +105,8 @@ def attn(lib, B=2, n=1, H=4, Hkv=2, d=64, dtype=BF16, scale=0.0, q=P[6], sq=(256
     (dict(table=None), INVALID), (dict(o=None), INVALID), (dict(o=P[9] + 8), MISALIGNED), (dict(lse=None), INVALID),
     (dict(width=0), INVALID), (dict(width=2 ** 25), INVALID), (dict(max_len=-1), INVALID), (dict(c=cache(page=8)), UNSUPPORTED),
     (dict(B=65536), INVALID), (dict(width=2 ** 60, stride=2 ** 60), INVALID), (dict(n=2 ** 25), INVALID),
-    (dict(H=65536), INVALID), (dict(c=cache(strides=(8192, 4096, 2 ** 32))), UNSUPPORTED)])
+    (dict(H=65536), INVALID), (dict(c=cache(strides=(8192, 4096, 2 ** 32))), UNSUPPORTED),
+    (dict(lens=P[7] + 2), MISALIGNED), (dict(table=P[8] + 1), MISALIGNED), (dict(lse=P[10] + 2), MISALIGNED)])
 def test_cache_attn_refuses(lib, bad, code):
     assert attn(lib, **bad) == code
 
@@ -119,7 +122,9 @@ def prompt(lib, T=8, H=4, Hkv=2, d=64, dtype=BF16, scale=0.0, q=P[0], sq=(512, 6
     (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(H=5), INVALID), (dict(Hkv=0), INVALID), (dict(d=80), UNSUPPORTED),
     (dict(dtype=F32), UNSUPPORTED), (dict(scale=float("nan")), INVALID), (dict(q=None), INVALID), (dict(k=P[1] + 2), MISALIGNED),
     (dict(v=None), INVALID), (dict(sv=(508, 64)), MISALIGNED), (dict(B=-1), INVALID), (dict(B=2 ** 21), INVALID),
-    (dict(starts=None), INVALID), (dict(o=None), INVALID), (dict(o=P[4] + 8), MISALIGNED), (dict(lse=None), INVALID)])
+    (dict(starts=None), INVALID), (dict(o=None), INVALID), (dict(o=P[4] + 8), MISALIGNED), (dict(lse=None), INVALID),
+    (dict(sk=(512, 0)), INVALID), (dict(sq=(0, 64)), INVALID), (dict(sv=(32, 64)), INVALID), (dict(starts=P[3] + 2), MISALIGNED),
+    (dict(lse=P[5] + 1), MISALIGNED)])
 def test_prompt_attn_refuses(lib, bad, code):
     assert prompt(lib, **bad) == code
 
