@@ -41,9 +41,7 @@ class Strides(ctypes.Structure):
     _fields_ = [("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
-# The other structs of the serving operators, as bytes (packing them costs a
-# fraction of what filling a ctypes.Structure does, and these calls are short):
-# shape (B, L, H, d, dtype, scale) and tokens (T, H, Hkv, d, dtype, scale),
+# The other structs of the serving operators, as bytes: shape (B, L, H, d, dtype, scale) and tokens (T, H, Hkv, d, dtype, scale),
 # rope_tables (cos, sin, n_positions, rot, layout), cache (k, v, k_scale,
 # v_scale, pages, page_tokens, three strides, two scale strides).
 pack_shape = pack_tokens = struct.Struct("@4qif").pack
@@ -157,6 +155,11 @@ def load(path: str = None) -> ctypes.CDLL:
         lib.attn_jvp_version.restype = ctypes.c_int32
         _lib = lib
         return lib
+
+
+def address(lib: ctypes.CDLL, name: str) -> int:
+    """Where a function of the library is, for callers that are not ctypes."""
+    return ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
 
 
 def status_string(code: int) -> str:

@@ -1,4 +1,5 @@
-"""Build the CUDA library libattn_jvp.so in-tree for sm_100a with nvcc.
+"""Build the CUDA library libattn_jvp.so in-tree for sm_100a with nvcc, and the
+Python binding of the serving operators, _serving.so, with the C++ compiler.
 
     python -m attention_jvp_attn_b200.build [--force] [--verbose]
 
@@ -13,12 +14,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libattn_jvp.so")
+BINDING = os.path.join(PKG, "_serving.so")
 # Opt-in variant whose bf16 kernel records per-tile event clocks of CTA 0.
 TRACE_LIB = os.path.join(PKG, "libattn_jvp_trace.so")
 
@@ -47,8 +50,42 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def _run(cmd, verbose: bool):
+    if verbose:
+        print(" ".join(cmd))
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+    return res.stdout + res.stderr
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """_serving.so: it reads torch tensors, so it is built against this torch,
+    and by the g++ that nvcc takes too: one with a C++ runtime of its own linked
+    in statically crashes beside torch's as soon as a message formats a number."""
+    src, header = os.path.join(CSRC, "serve_binding.cpp"), os.path.join(INCLUDE, "attn_jvp.h")
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in (src, header)):
+        return BINDING
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    includes = [INCLUDE, os.path.join(at, "include"), os.path.join(at, "include/torch/csrc/api/include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    out = _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                *(f for i in includes for f in ("-isystem", i)), "-o", BINDING + ".tmp", src,
+                "-L" + os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], verbose)
+    if verbose:
+        sys.stdout.write(out)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
           trace: bool = False) -> str:
+    if not trace:
+        build_binding(force, verbose)
     lib = TRACE_LIB if trace else LIB
     if not force and up_to_date(lib):
         return lib
@@ -57,13 +94,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
            *(["-DAJVP_TRACE"] if trace else []), "-o", lib + ".tmp", *_sources()]
     if ptxas_info:
         cmd[1:1] = ["-Xptxas", "-v"]
-    if verbose:
-        print(" ".join(cmd))
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+    out = _run(cmd, verbose)
     if verbose or ptxas_info:
-        sys.stdout.write(res.stdout + res.stderr)
+        sys.stdout.write(out)
     os.replace(lib + ".tmp", lib)
     return lib
 

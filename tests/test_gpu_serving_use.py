@@ -268,6 +268,36 @@ def test_empty_calls():
 
 
 # ------------------------------------------------------------------ refusals
+def test_forms_of_out_and_scale():
+    """`out` is any pair and comes back as it was given; a scale is a number that 32 bits hold."""
+    g = rng(12)
+    q, k = randn(g, 3, 2, 64), randn(g, 3, 1, 64)
+    cos, sin = aj.rope_tables(64, 8)
+    at = ints([0, 5, 7])
+    want = aj.rope_at(q, k, at, cos, sin)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    got = aj.rope_at(q, k, at, cos, sin, out=[qo, ko])
+    assert got[0] is qo and got[1] is ko and torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+    only = aj.rope_at(q, None, at.long(), cos, sin)
+    assert only[1] is None and torch.equal(only[0], want[0])
+    got = aj.rope_at(q, None, at, cos, sin, out=(qo, None))
+    assert got[0] is qo and got[1] is None
+    for out in ((qo,), (qo, ko, qo), (qo, None), (ko, qo), (qo[:2], ko), (qo.float(), ko), 3):
+        with pytest.raises((ValueError, TypeError)):
+            aj.rope_at(q, k, at, cos, sin, out=out)
+    starts = ints([0, 3])
+    o, lse = aj.prompt_attn(q, k, k, starts, scale=1)
+    mine = torch.empty_like(o), torch.empty_like(lse)
+    got = aj.prompt_attn(q, k, k, starts, scale=np.float64(1.0), out=mine)
+    assert got[0] is mine[0] and got[1] is mine[1] and torch.equal(mine[0], o) and torch.equal(mine[1], lse)
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 1e-60, 1e60, "1"):
+        with pytest.raises((ValueError, TypeError)):
+            aj.prompt_attn(q, k, k, starts, scale=scale)
+    with pytest.raises(TypeError):
+        aj.prompt_attn(q.float(), k.float(), k.float(), starts)
+    ok()
+
+
 def test_wrong_arguments_are_refused():
     """Calls that need tensors on the GPU to be refused; nothing is launched."""
     g = rng(8)

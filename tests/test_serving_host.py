@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import attention_jvp_attn_b200 as aj
-from attention_jvp_attn_b200 import _abi, serving
+from attention_jvp_attn_b200 import _abi
 from oracle import serving_oracle as orc
 
 BF16, F32, F16 = _abi.DTYPE_BF16, _abi.DTYPE_F32, _abi.DTYPE_F16
@@ -149,7 +149,7 @@ def test_status_string(lib):
 
 
 # ------------------------------------------------------------------ the wrapper
-def test_wrapper_refuses_host_tensors():
+def test_wrapper_refuses_host_tensors(lib):
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     i = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
@@ -162,6 +162,37 @@ def test_wrapper_refuses_host_tensors():
         aj.cache_append(aj.paged_cache(2, 16, 2, 64, device="cpu"), x, x, i, i, i)
     with pytest.raises(ValueError, match=r"\[T, heads, d\]"):
         aj.rope_at(x[0], None, i, x, x)
+
+
+def test_wrapper_refuses_what_is_no_tensor(lib):
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(4, dtype=torch.int32)
+    c = aj.paged_cache(2, 16, 2, 64, device="cpu")
+    for call in (lambda: aj.rope_at(None, x, i, x, x), lambda: aj.rope_at([1], x, i, x, x),
+                 lambda: aj.cache_attn(3, c, i, i), lambda: aj.cache_append(c[:3], x, x, i, i, i),
+                 lambda: aj.cache_append(None, x, x, i, i, i), lambda: aj.cache_append(c, x, 1.0, i, i, i),
+                 lambda: aj.prompt_attn(x, x, None, i)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_binding_shares_the_process_cpp_runtime(lib):
+    """Two C++ runtimes in one process crash when a message formats a number."""
+    from attention_jvp_attn_b200 import build
+    with open(build.BINDING, "rb") as f:
+        assert b"\0libstdc++.so.6\0" in f.read()
+
+
+def test_missing_binding_fails_loudly(lib, monkeypatch):
+    """Without its binding an operator raises; nothing stands in for it."""
+    import sys
+    from attention_jvp_attn_b200 import serving
+    monkeypatch.setattr(serving, "_bound", None)
+    monkeypatch.delattr(aj, "_serving", raising=False)
+    monkeypatch.setitem(sys.modules, "attention_jvp_attn_b200._serving", None)
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(RuntimeError, match="not built"):
+        aj.prompt_attn(x, x, x, x)
 
 
 @pytest.mark.parametrize("args", [(2, 24, 1, 64), (2, 16, 1, 96), (0, 16, 1, 64), (2, 16, 0, 64)])
@@ -238,7 +269,3 @@ def test_oracle_rope_pins():
     inter = orc.rope(x, [0], cos, sin, "interleaved")[0, 0]
     assert (inter[0::2] == -x[0, 0, 1::2]).all() and (inter[1::2] == x[0, 0, 0::2]).all()
     assert np.allclose(orc.rope(orc.rope(x, [0], cos, sin, "half"), [0], cos, sin, "half", True), x)
-
-
-def test_strides_are_shared_by_value():
-    assert serving._strides(128, 64).token == 128 and serving._strides(64, 128).token == 64
