@@ -51,6 +51,7 @@ namespace {
 
 constexpr int kRowsWarps = 4;
 constexpr int kStep = 32;                  // tokens per step of a warp
+constexpr int kMostSplits = 8;             // blocks of a cluster
 constexpr int kLeastSteps = 8;             // steps of a block: two of a warp
 constexpr uint32_t kHidden = 0xffffffffu;  // in place of a key scale: no page there
 
@@ -615,17 +616,26 @@ __global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_k
     for (int item = rank + threadIdx.x * p.splits; item < C::ROWS * (D / 4); item += kThreads * p.splits) {
       const int r = item / (D / 4), col = (item % (D / 4)) * 4;
       if (r >= rows) continue;
-      float top = -INFINITY, sum = 0.f;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < p.splits; ++k)
-        top = fmaxf(top, ld_cluster_f32(ajvp::mapa_shared(bm_addr + r * 4, k)));
-      for (int k = 0; k < p.splits; ++k) {
-        const float mk = ld_cluster_f32(ajvp::mapa_shared(bm_addr + r * 4, k));
-        const float f = top == -INFINITY ? 1.f : ajvp::ex2_approx(mk - top);
-        sum = fmaf(ld_cluster_f32(ajvp::mapa_shared(bm_addr + (C::ROWS + r) * 4, k)), f, sum);
-        const float4 z = ld_cluster_f32x4(ajvp::mapa_shared(sums_addr + (r * C::PITCH + col) * 4, k));
-        y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y);
-        y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
+      // all blocks' reads are in flight together
+      float mk[kMostSplits], lk[kMostSplits], top = -INFINITY, sum = 0.f;
+      float4 z[kMostSplits], y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMostSplits; ++k) {
+        mk[k] = -INFINITY, lk[k] = 0.f, z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < p.splits) {
+          mk[k] = ld_cluster_f32(ajvp::mapa_shared(bm_addr + r * 4, k));
+          lk[k] = ld_cluster_f32(ajvp::mapa_shared(bm_addr + (C::ROWS + r) * 4, k));
+          z[k] = ld_cluster_f32x4(ajvp::mapa_shared(sums_addr + (r * C::PITCH + col) * 4, k));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kMostSplits; ++k) top = fmaxf(top, mk[k]);
+#pragma unroll
+      for (int k = 0; k < kMostSplits; ++k) {
+        const float f = top == -INFINITY ? 1.f : ajvp::ex2_approx(mk[k] - top);
+        sum = fmaf(lk[k], f, sum);
+        y.x = fmaf(z[k].x, f, y.x), y.y = fmaf(z[k].y, f, y.y);
+        y.z = fmaf(z[k].z, f, y.z), y.w = fmaf(z[k].w, f, y.w);
       }
       write_row<T, D>(p, b, hk, r, col, y, top, sum);
     }
@@ -854,7 +864,7 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
     if (!workspace || workspace_bytes < share.blocks * share.bytes) return ATTN_JVP_ERR_INVALID_ARGUMENT;
     if (!aligned16(workspace)) return ATTN_JVP_ERR_MISALIGNED;
   } else {
-    while (p.splits < 8 && tiles * p.splits < 2 * sms && len >= 256 * p.splits) p.splits *= 2;
+    while (p.splits < kMostSplits && tiles * p.splits < 2 * sms && len >= 256 * p.splits) p.splits *= 2;
   }
   rp.work = share.blocks ? static_cast<float*>(workspace) : nullptr;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
