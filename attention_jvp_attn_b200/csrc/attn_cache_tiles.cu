@@ -522,8 +522,6 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
           u[k] = *reinterpret_cast<const uint4*>(D == 128 ? smem_xor(from + block * 1024, (k % CH) << 6)
                                                           : from + block * 512);
         }
-        __syncwarp();
-        mbar_arrive_if(&raw_empty[st], lane == 0);
         if (!wwait(&empty[slot], ((run / C::NS) & 1) ^ 1)) break;
         uint8_t* to = sRing + slot * C::TILE;
 #pragma unroll
@@ -541,6 +539,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
         fence_proxy_async_shared();
         __syncwarp();
         mbar_arrive_if(&full[slot], lane == 0);
+        // The stage is given back only here, where its codes have been stored: the
+        // assembler may move reads that nothing has used yet behind the arrival
+        // and the wait for the slot, and then they see the next copy.
+        mbar_arrive_if(&raw_empty[st], lane == 0);
       }
       __syncwarp();
       mbar_arrive_if(loaded, lane == 0);

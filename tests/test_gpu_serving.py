@@ -408,3 +408,20 @@ def test_prompt_attn(lens, before, behind, H, Hkv, d, dtype):
         assert (o[rows] == 5).all() and (lse[:, rows] == 6).all()
     again = aj.prompt_attn(q, k, v, ints(starts), scale=scale)
     assert torch.equal(o[a:e], again[0][a:e]) and torch.equal(lse[:, a:e], again[1][:, a:e])
+
+
+@pytest.mark.parametrize("seqs,n,H,Hkv", [(27, 21, 2, 1), (10, 117, 2, 2), (2, 57, 4, 2)])
+def test_cache_attn_repeats(seqs, n, H, Hkv):
+    """One row tile of d = 128, the keys ready before their turn: each of many calls
+    gives the first one's bits."""
+    g = rng(seqs)
+    lens = [900 + 131 * b for b in range(seqs)]
+    pages = sum(-(-m // 32) for m in lens) + 2
+    cache = filled(g, pages, Hkv, 32, 128)
+    table = tables(g, pages, lens, 32)
+    q = randn(g, seqs, n, H, 128, dtype=torch.float16)
+    first = aj.cache_attn(q, cache, ints(lens), table)
+    for _ in range(100):
+        o, lse = aj.cache_attn(q, cache, ints(lens), table)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    ok()
