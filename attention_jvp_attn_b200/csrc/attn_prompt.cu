@@ -23,7 +23,7 @@
 // tile's probabilities is handed to the products before the second half is
 // formed. Measured (one B200, bf16): 32,760 tokens, 8 query and 2 key heads, d =
 // 128: 1.52 to 1.82 ms, 1,210 to 1,440 TFLOP/s by the power-capped clock; five
-// prompts of 61 to 8,192 tokens: 0.56 to 0.66 ms; 1,333 tokens, d = 64: 22.5 us. A
+// prompts of 61 to 8,192 tokens: 0.56 to 0.66 ms; 1,333 tokens, d = 64: 17.3 us. A
 // pair of key tiles takes 3,200 cycles, 2,048 of them tensor work.
 //
 // A masked key's probability is 0, but 0 times an infinity or NaN among its
@@ -63,7 +63,7 @@ struct PromptCfg {
   static constexpr int TILE = kTile * D * 2;
   static constexpr int NS = D == 128 ? 5 : 10;  // ring slots, K and V tiles in turn
   static constexpr int DATA = (2 + NS) * TILE;
-  static constexpr int NBAR = 2 * NS + 7 * 2 + 1;
+  static constexpr int NBAR = 2 * NS + 7 * 2 + 2;
   static constexpr int BYTES = 1024 + DATA + NBAR * 8 + 2 * 4 * 4 + 16;
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S_t at 128 t, O_t at 256 + D t
   static_assert(BYTES <= 232448, "shared memory budget");
@@ -76,26 +76,26 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
              : (((w & 0x7f807f80u) + 0x00800080u) >> 15) & 0x00010001u;
 }
 
-// The rank-th pair of row tiles of all sequences: its sequence b and its index
-// k in it. Up to kThreads sequences: those that see the most keys first, so
-// that the blocks started last are short whatever the sequences' order. Pairs
+// The rank-th block of `unit` query rows (a "pair" of row tiles below) of all
+// sequences: its sequence b and its index k in it. Up to kThreads sequences:
+// those that see the most keys first, so that the blocks started last are short whatever the sequences' order. Pairs
 // of index k or above number sum_b max(0, pairs(b) - k), so k is found by
 // bisection and b among the sequences that have a pair k: one round of loads
-// and log2 (T / 256) sums over the block. More sequences: in their order, by
+// and log2 (T / unit) sums over the block. More sequences: in their order, by
 // find_sequence. Every thread of the block calls this; false if there is no
 // such pair.
-__device__ __forceinline__ bool find_pair(const PromptParams& p, int rank, int& b, int& k) {
+__device__ __forceinline__ bool find_pair(const PromptParams& p, int unit, int rank, int& b, int& k) {
   __shared__ int sums[kThreads / 32];
   __shared__ int found;
   auto pairs = [&](int i) -> int {
     const int raw0 = p.starts[i], raw1 = p.starts[i + 1];
     const int t0 = clamp_row(raw0, p.T), t1 = clamp_row(raw1, p.T);
     if (t0 != raw0 || t1 != raw1 || t1 < t0) atomicOr(p.status, kStatusBadIndex);
-    return t1 > t0 ? (t1 - t0 + 2 * kTile - 1) / (2 * kTile) : 0;
+    return t1 > t0 ? (t1 - t0 + unit - 1) / unit : 0;
   };
   if (p.B > kThreads) {
-    b = find_sequence(p.starts, p.B, p.T, 2 * kTile, 1, rank);
-    k = rank - (clamp_row(p.starts[b], p.T) / (2 * kTile) + b);
+    b = find_sequence(p.starts, p.B, p.T, unit, 1, rank);
+    k = rank - (clamp_row(p.starts[b], p.T) / unit + b);
     return k >= 0 && k < pairs(b);
   }
   const int warp = threadIdx.x >> 5;
@@ -111,7 +111,7 @@ __device__ __forceinline__ bool find_pair(const PromptParams& p, int rank, int& 
     return x;
   };
   auto from = [&](int at) { return total(max(own - at, 0)); };  // pairs of index `at` or above
-  int lo = 0, hi = p.T / (2 * kTile) + 1;  // from(lo) > rank >= from(hi)
+  int lo = 0, hi = p.T / unit + 1;  // from(lo) > rank >= from(hi)
   int above = 0;
   if (from(0) <= rank) return false;
   while (hi - lo > 1) {
@@ -136,7 +136,11 @@ __device__ __forceinline__ bool find_pair(const PromptParams& p, int rank, int& 
   return true;
 }
 
-template <int D, bool F16>
+// SINGLE: the block has one row tile, whose key tiles are taken in turn by the
+// two sets of scores, softmax warps and sums that otherwise belong to two row
+// tiles ("t" below: row tile, or key tiles 2 i + t); their sums are joined at the
+// end.
+template <int D, bool F16, bool SINGLE>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
   using C = PromptCfg<D>;
   using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
@@ -156,25 +160,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   uint64_t* clean = q_full + 8;       // [2] values of a diagonal tile looked through
   uint64_t* sent = q_full + 10;       // [2] the copy of a diagonal tile's values is on its way
   uint64_t* drain = q_full + 14;
+  uint64_t* joined = q_full + 15;     // SINGLE: the second set's sums and statistics
   uint32_t* marked = reinterpret_cast<uint32_t*>(bars + C::NBAR);  // [2][4] keys with non-finite values
   uint32_t* tmem_slot = marked + 8;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
+  constexpr int unit = SINGLE ? kTile : 2 * kTile;
   const int head = blockIdx.x % p.H;
   __shared__ int where[2];
   {
     int b, block;
-    if (!find_pair(p, static_cast<int>(blockIdx.x / p.H), b, block)) return;
+    if (!find_pair(p, unit, static_cast<int>(blockIdx.x / p.H), b, block)) return;
     if (threadIdx.x == 0) where[0] = b, where[1] = block;
     __syncthreads();
   }
   const int b = where[0], block = where[1];
   const int t0 = clamp_row(p.starts[b], p.T), t1 = clamp_row(p.starts[b + 1], p.T);
-  const int first = block * 2 * kTile;  // the pair's first row
+  const int first = block * unit;  // the block's first row
   const int len = t1 - t0;
   // Key tiles of the two row tiles; the last one of each is on its diagonal.
-  const int n0 = 2 * block + 1;
-  const int n1 = first + kTile < len ? n0 + 1 : 0;
+  const int n0 = first / kTile + 1;
+  const int n1 = !SINGLE && first + kTile < len ? n0 + 1 : 0;
   const int n = n1 ? n1 : n0;
 
   const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5));
@@ -197,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_init(&sent[i], 1);
     }
     mbar_init(drain, 1);
+    mbar_init(joined, 4);
     for (int i = 0; i < 8; ++i) marked[i] = 0;
     *abort_flag = 0;
     fence_barrier_init();
@@ -262,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       auto slot_addr = [&](int i) { return aR + (i % C::NS) * C::TILE; };
       auto landed = [&](int i) { return wwait(&full[i % C::NS], (i / C::NS) & 1); };
       auto scores = [&](int t, int j) {
-        mma_scores<D, kTile, kTile, false>(tmem + C::TM_S + kTile * t, aQ + t * C::TILE,
+        mma_scores<D, kTile, kTile, false>(tmem + C::TM_S + kTile * t, aQ + (SINGLE ? 0 : t * C::TILE),
                                            slot_addr(2 * j), idesc_s, false);
         umma_commit(&s_full[t]);
       };
@@ -276,35 +283,42 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (ok) scores(1, 0);
         }
         umma_commit(&empty[0]);
+        if (SINGLE && n > 1) {
+          ok = landed(2);
+          tc_fence_after();
+          if (ok) scores(1, 1);
+          umma_commit(&empty[2]);
+        }
       }
       // Per key tile j and row tile t: O_t += P_t V_j, then the next scores
       // over P_t (one thread's products execute in order), which the softmax
       // of row tile t turns into probabilities beside the other row tile's
       // products.
       for (int j = 0; ok && j < n; ++j) {
-        const int vi = 2 * j + 1, ki = 2 * j + 2;
+        const int vi = 2 * j + 1, ahead = SINGLE ? 2 : 1, ki = 2 * (j + ahead);
         ok = landed(vi) && (j < n0 - 1 || wwait(&clean[j - (n0 - 1)], 0));
         for (int t = 0; ok && t < 2; ++t) {
-          const int nt = t ? n1 : n0;
-          if (j >= nt) continue;
-          ok = wwait(&p_full[t], j & 1);
+          const int nt = !SINGLE && t ? n1 : n0;
+          if (SINGLE ? t != (j & 1) : j >= nt) continue;
+          const int phase = SINGLE ? (j >> 1) & 1 : j & 1;
+          ok = wwait(&p_full[t], phase);
           if (!ok) break;
           tc_fence_after();
           mma_values_half<D, 0>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi),
-                                idesc_v, j > 0);
+                                idesc_v, SINGLE ? j > 1 : j > 0);
           // the next keys, while the second half's probabilities are formed
-          if (j + 1 < nt) ok = landed(ki);
-          ok = ok && wwait(&p_late[t], j & 1);
+          if (j + ahead < nt) ok = landed(ki);
+          ok = ok && wwait(&p_late[t], phase);
           if (!ok) break;
           tc_fence_after();
           mma_values_half<D, 1>(tmem + C::TM_O + D * t, tmem + C::TM_S + kTile * t, slot_addr(vi),
                                 idesc_v, true);
           umma_commit(&pv_done[t]);
-          if (j + 1 < nt) scores(t, j + 1);
+          if (j + ahead < nt) scores(t, j + ahead);
         }
         if (!ok) break;
         umma_commit(&empty[vi % C::NS]);
-        if (j + 1 < n) umma_commit(&empty[ki % C::NS]);
+        if (j + ahead < n) umma_commit(&empty[ki % C::NS]);
       }
       umma_commit(drain);  // every product ends before tensor memory is released
       if (lane == 0) mbar_wait_drain(drain, 0, 1000000000ull);
@@ -349,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     setmaxnreg_inc<208>();
     const int t = warp >> 2, sub = warp & 3;
     const int row = sub * 32 + lane;
-    const int nt = t ? n1 : n0;
+    const int nt = SINGLE ? (n0 + 1 - t) / 2 : t ? n1 : n0;
     const uint32_t lane_off = static_cast<uint32_t>(sub * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::TM_S + kTile * t;
     const uint32_t tO = tmem + lane_off + C::TM_O + D * t;
@@ -371,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       for (int x = 0; x < kTile; x += 32)
         tmem_ld32(tS + x, *reinterpret_cast<uint32_t(*)[32]>(&s[x]));
       tmem_wait_ld();
-      if (j == nt - 1) {
+      if (SINGLE ? 2 * j + t == n0 - 1 : j == nt - 1) {
 #pragma unroll
         for (int x = 0; x < kTile; ++x)
           if (x > row) s[x] = __float_as_uint(-INFINITY);
@@ -403,11 +417,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_arrive_if(&p_late[t], lane == 0);
       l += sum.x + sum.y;
     }
-    if (ok && nt > 0 && wwait(&pv_done[t], (nt - 1) & 1) && wwait(&clean[0], 0) &&
-        (t == 0 || wwait(&clean[1], 0))) {
+    bool writes = nt > 0;
+    float* stats = reinterpret_cast<float*>(sQ + C::TILE);  // SINGLE: m and l of the second set
+    if (SINGLE && t == 1) {
+      writes = false;
+      if (ok && (nt == 0 || wwait(&pv_done[1], (nt - 1) & 1))) {
+        tc_fence_after();
+        stats[row] = m, stats[kTile + row] = l;
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_if(joined, lane == 0);
+      }
+    }
+    if (ok && writes && wwait(&pv_done[t], (nt - 1) & 1) && wwait(&clean[0], 0) &&
+        (t == 0 || wwait(&clean[1], 0)) && (!SINGLE || wwait(joined, 0))) {
       tc_fence_after();
-      const int r = first + t * kTile + row;  // row of the sequence
+      const int r = first + (SINGLE ? 0 : t * kTile) + row;  // row of the sequence
       const bool mine = r < len;
+      float f0 = 1.f, f1 = 0.f;
+      if (SINGLE && n0 > 1) {
+        const float other = stats[row], to = fmaxf(m, other);
+        f0 = to == -INFINITY ? 1.f : ex2_approx(m - to);
+        f1 = to == -INFINITY ? 1.f : ex2_approx(other - to);
+        m = to;
+        l = l * f0 + stats[kTile + row] * f1;
+      }
       const float inv = 1.f / l;
       // keys with non-finite values that this row sees: all marked ones of the
       // first diagonal tile up to the row, or of the second too
@@ -420,6 +454,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         uint32_t y[32];
         tmem_ld32(tO + x, y);
         tmem_wait_ld();
+        if (SINGLE && n0 > 1) {
+          uint32_t z[32];
+          tmem_ld32(tO + D + x, z);  // the second set's, in the same lanes
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            y[c] = __float_as_uint(__uint_as_float(y[c]) * f0 + __uint_as_float(z[c]) * f1);
+        }
         if (any && mine) {
           for (int k = 0; k < (t + 1) * kTile; ++k) {
             const int key = first + k;
@@ -454,12 +496,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   if (warp == 9) tmem_dealloc(tmem, C::TM_COLS);
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool SINGLE>
 cudaError_t prompt_launch(const PromptParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(prompt_kernel<D, F16>, PromptCfg<D>::BYTES, done);
+  const cudaError_t e = allow_smem(prompt_kernel<D, F16, SINGLE>, PromptCfg<D>::BYTES, done);
   if (e != cudaSuccess) return e;
-  prompt_kernel<D, F16><<<p.pieces * p.H, kThreads, PromptCfg<D>::BYTES, st>>>(p);
+  prompt_kernel<D, F16, SINGLE><<<p.pieces * p.H, kThreads, PromptCfg<D>::BYTES, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -488,10 +530,11 @@ extern "C" int attn_jvp_prompt_attn(const attn_jvp_tokens* shape, const void* q,
       (rc = check_rows_map(k, k_strides, s.T, s.Hkv, s.d, 2)) != ATTN_JVP_OK ||
       (rc = check_rows_map(v, v_strides, s.T, s.Hkv, s.d, 2)) != ATTN_JVP_OK)
     return rc;
-  const int64_t pieces = s.T / (2 * kTile) + B;
+  int64_t pieces = s.T / (2 * kTile) + B;
   if (pieces * s.H > (int64_t(1) << 30)) return ATTN_JVP_ERR_UNSUPPORTED;
   PromptParams p;
-  rc = ajvp::device_status_word(&p.status);
+  int sms = 0;
+  rc = ajvp::device_status_word(&p.status, &sms);
   if (rc != ATTN_JVP_OK) return rc;
   if (!ajvp::encode_token_rows_map(&p.map_q, q, s.dtype, s.T, s.H, s.d, q_strides.token,
                                    q_strides.head, kTile) ||
@@ -504,14 +547,23 @@ extern "C" int attn_jvp_prompt_attn(const attn_jvp_tokens* shape, const void* q,
   p.o = o, p.lse = lse, p.starts = starts;
   p.T = static_cast<int>(s.T), p.B = static_cast<int>(B), p.H = static_cast<int>(s.H);
   p.group = static_cast<int>(s.H / s.Hkv);
+  // Blocks of one row tile where blocks of two would not fill the SMs (they read
+  // each key twice as often). us, one / two, d = 64, by length and heads:
+  //   300 x 4: 8.6 / 9.2    1,333 x 16: 17.3 / 21.7   4,000 x 8: 34.8 / 54.8   8,000 x 4: 53.6 / 99.8
+  //   2,600 x 16: 39.3 / 37.4   4,000 x 16: 68.2 / 58.2   8 of 500, 8 heads: 17.7 / 13.8
+  const bool single = pieces * s.H <= sms;
+  if (single) pieces = s.T / kTile + B;
   p.pieces = static_cast<int>(pieces);
   const float scale = s.scale > 0.f ? s.scale : 1.0f / std::sqrt(static_cast<float>(s.d));
   p.scale_log2 = scale * 1.4426950408889634f;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (s.dtype == ATTN_JVP_BF16)
-    e = s.d == 128 ? prompt_launch<128, false>(p, st) : prompt_launch<64, false>(p, st);
-  else
-    e = s.d == 128 ? prompt_launch<128, true>(p, st) : prompt_launch<64, true>(p, st);
+  auto launch = [&](auto one) {
+    constexpr bool S = decltype(one)::value;
+    if (s.dtype == ATTN_JVP_BF16)
+      return s.d == 128 ? prompt_launch<128, false, S>(p, st) : prompt_launch<64, false, S>(p, st);
+    return s.d == 128 ? prompt_launch<128, true, S>(p, st) : prompt_launch<64, true, S>(p, st);
+  };
+  e = single ? launch(std::true_type()) : launch(std::false_type());
   return e == cudaSuccess ? ATTN_JVP_OK : ATTN_JVP_ERR_CUDA;
 }

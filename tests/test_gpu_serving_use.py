@@ -233,6 +233,43 @@ def test_cache_attn_bad_indices(n, H, width):
         assert torch.allclose(lse, want[1], rtol=1e-5, atol=1e-5)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+def test_prompt_blocks_of_one_and_two_row_tiles(d, dtype):
+    """Many heads take blocks of two row tiles, few heads blocks of one; both against
+    the oracle over sequences that end inside, at and behind tiles, and with values
+    that are not finite in their last rows, which earlier rows must not meet."""
+    g = rng(d + 3)
+    lens = [300, 1, 257, 128, 0, 129, 511]
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    T, H, few = int(starts[-1]), 64, 4  # 64 heads: more than 800 pairs of row tiles
+    q, k, v = randn(g, T, H, d, dtype=dtype), randn(g, T, 2, d, dtype=dtype), randn(g, T, 2, d, dtype=dtype)
+    u = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -11
+    scale = 0.7 / np.sqrt(d)
+    ref = orc.prompt_attn(f64(q[:, 30:34]), f64(k), f64(v), starts, scale)  # two heads of each key head
+    qf = q[:, 30:34].contiguous()
+    outs = {}
+    for bad in (False, True):
+        if bad:
+            v = v.clone()
+            for e in starts[1:]:
+                v[e - 1, :, 3] = NAN
+                v[max(e - 2, 0), :, 5] = INF
+        many = aj.prompt_attn(q, k, v, ints(starts), scale=scale)
+        one = aj.prompt_attn(qf, k, v, ints(starts), scale=scale)
+        ok()
+        outs[bad] = (many[0][:, 30:34], many[1][30:34]), one
+    for o, lse in outs[False]:
+        check_attn(o, lse, qf, ref, scale, u)
+    for (o, lse), (good, same_lse) in zip(outs[True], outs[False]):
+        met = torch.zeros(T, d, dtype=torch.bool, device="cuda")
+        for a, e in zip(starts, starts[1:]):
+            met[a:e] = (~torch.isfinite(v[a:e, 0])).cumsum(0) > 0
+        assert torch.equal(lse, same_lse)
+        keep = ~met[:, None].expand_as(o)
+        assert torch.equal(o[keep], good[keep])
+        assert not torch.isfinite(o[~keep]).any()
+
+
 def test_prompt_bad_starts():
     g = rng(6)
     q, k, v = (randn(g, 50, h, 64) for h in (2, 1, 1))
