@@ -78,8 +78,8 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
 
 // The rank-th block of `unit` query rows (a "pair" of row tiles below) of all
 // sequences: its sequence b and its index k in it. Up to kThreads sequences:
-// those that see the most keys first, so that the blocks started last are short whatever the sequences' order. Pairs
-// of index k or above number sum_b max(0, pairs(b) - k), so k is found by
+// those that see the most keys first, so that the blocks started last are short
+// whatever the sequences' order. Pairs of index k or above number sum_b max(0, pairs(b) - k), so k is found by
 // bisection and b among the sequences that have a pair k: one round of loads
 // and log2 (T / unit) sums over the block. More sequences: in their order, by
 // find_sequence. Every thread of the block calls this; false if there is no
