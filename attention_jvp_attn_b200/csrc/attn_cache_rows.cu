@@ -5,10 +5,14 @@
 // page scales a_j, b_j:
 //   x_j = s a_j <q, k_j>,  O = sum_j e^(x_j) b_j v_j / sum_j e^(x_j)
 // One pass with a running maximum, in powers of two. The value scale goes into
-// the exponent: with t_j = x_j log2 e + log2 b_j and m = max t_j,
+// the exponent: with t_j = x_j log2 e + log2 b_j and m near max t_j (kLead),
 //   p_j = 2^(t_j - m),  O = sum_j p_j v_j / sum_j p_j / b_j,
-// so p is at most 2^kLazyMax however the scales differ, and what fp16 rounds
-// away of p is small against the largest contribution to O.
+// so p is at most 2^kRaise however the scales differ. What fp16 takes from a p_j,
+// 2^-11 of it or 2^-32 of the row's largest p, is small against the largest e^x b,
+// a bound on a contribution to O, not a contribution: where the page of the
+// largest holds codes near 0 (one token of the page is far larger than the others)
+// and the other pages' scales are below some 2^-20 of its own, O is made of
+// probabilities of few bits. The sum of p / b is of the unrounded ones.
 //
 // Bound by HBM: a cached token is 2 d bytes per key head, read once; the rows
 // (all query heads of the key head, and the newest tokens) share it. Codes are
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_k
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) raise |= top[t][i] > m[t][i] + kLazyMax;
+        for (int i = 0; i < 2; ++i) raise |= top[t][i] > m[t][i] + kRaise;
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_k
             to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 4));
             to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 8));
             to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 16));
-            to = fmaxf(to, m[t][i]);
+            to = fmaxf(to - kLead, m[t][i]);
             const float f = to == -INFINITY ? 1.f : ajvp::ex2_approx(m[t][i] - to);
             m[t][i] = to;
             l[t][i] *= f;

@@ -632,8 +632,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
             const Groups gr(sc + 4 * h, row_scale);
             const float top = max_groups(s, gr);
             add = exp_groups(s, gr, m, pk);
-            if (!__any_sync(0xffffffffu, top > m + kLazyMax)) break;
-            const float to = fmaxf(m, top);
+            if (!__any_sync(0xffffffffu, top > m + kRaise)) break;
+            const float to = fmaxf(m, top - kLead);
             const float f = to == -INFINITY ? 1.f : ex2_approx(m - to);
             m = to;
             l *= f;

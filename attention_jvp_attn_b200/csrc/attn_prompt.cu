@@ -5,7 +5,7 @@
 //   x_j = s <q_t, k_j>,  O_t = sum_j e^(x_j) v_j / sum_j e^(x_j),  j <= t
 // in one pass over the keys with a running maximum (the standard online
 // softmax; statistics and sums in fp32, the probabilities rounded to the
-// inputs' type for the second product, at most 2^kLazyMax).
+// inputs' type for the second product, at most 2^kRaise).
 //
 // Bound by the tensor cores (4 d operations per pair) and, about as much, by
 // the exponentials: a tile of 128 x 128 scores takes 1,024 cycles of MMA at
@@ -43,7 +43,6 @@ using namespace ajvp;
 
 constexpr int kThreads = 384;
 constexpr float kLn2F = 0.6931471805599453f;
-constexpr float kRaise = 8.f;  // the maximum is raised in steps above 2^8: see kLazyMax
 
 struct PromptParams {
   CUtensorMap map_q, map_k, map_v;  // (d, heads, T), boxes of 64 columns x 128 tokens
@@ -398,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       exp_half<F16>(&s[0], sc2, m, pk, sum);
       const float top = max128(s) * sc;
       if (__any_sync(0xffffffffu, top > m + kRaise)) {
-        const float to = fmaxf(m, top);
+        const float to = fmaxf(m, top - kLead);
         const float f = to == -INFINITY ? 1.f : ex2_approx(m - to);
         m = to;
         l *= f;

@@ -29,10 +29,6 @@ struct CacheAttnParams {
 constexpr float kMinScale = 9.094947017729282e-13f;  // 2^-40
 constexpr float kMaxScale = 1.099511627776e12f;      // 2^40
 constexpr float kLn2 = 0.6931471805599453f;
-// The running maximum is raised only when a score exceeds it by more than
-// this many powers of two, so accumulators are rarely rescaled; p <= 2^8
-// stays well inside fp16 and fp32.
-constexpr float kLazyMax = 8.f;
 
 __device__ __forceinline__ float read_scale(float s) {
   return fminf(fmaxf(s, kMinScale), kMaxScale);  // a NaN reads as the smallest

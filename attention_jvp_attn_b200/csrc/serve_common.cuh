@@ -86,6 +86,16 @@ inline int check_cache(const attn_jvp_cache* c, int64_t Hkv, int64_t d) {
   return ATTN_JVP_OK;
 }
 
+// The running maximum m of a row's exponents (in powers of two) is kept kLead
+// below the largest one at the time that it was raised, and raised again only
+// when one exceeds it by more than kRaise, so that the sums are rarely rescaled.
+// So probabilities 2^(t - m) are at most 2^15, which fp16 holds, and the row's
+// largest is 2^kLead or more: fp16 rounds one by 2^-11 of itself, or by 2^-25,
+// which is 2^-32 of the largest at most. At the largest itself (m = max t) the
+// bits between 1 and 65,504 would lie idle and 2^-25 of the largest be lost.
+constexpr float kLead = 7.f;
+constexpr float kRaise = 15.f;
+
 // Raises a kernel's shared-memory limit once per device (`done`: devices that
 // have it; the kernel's own).
 template <typename F>

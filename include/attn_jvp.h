@@ -615,6 +615,12 @@ int attn_jvp_cache_append(const attn_jvp_tokens* shape, const void* k, attn_jvp_
  *           one each
  *   o       [B, n, H, d] dense, of dtype;  lse [B, H, n] float dense
  *
+ * Sums, maxima and LSE are in 32 bits; e^(x_j) b_j, b_j being the value scale of
+ * key j's page, is held in fp16, the row's largest at 2^7 or more: each is off by
+ * at most 2^-11 of itself, or by 2^-32 of the row's largest, and counts as 0 from
+ * there down. Value scales of a head that differ by more than some 2^20 reach that
+ * limit if the values that count lie on the pages of small scale.
+ *
  * Scales in the cache are read as at least 2^-40 and at most 2^40. A sequence
  * whose length is out of range gets the empty row's result, and the tokens of
  * a page whose number is out of range count as hidden.
@@ -635,7 +641,8 @@ int64_t attn_jvp_cache_attn_workspace_bytes(const attn_jvp_shape* shape, int64_t
  * rows starts[b] <= t < starts[b + 1] of q, k and v, query t seeing keys
  * starts[b] <= j <= t. Nothing outside a row's keys reaches it, infinities
  * and NaN in masked rows included. Rows outside the sequences are left as
- * they were.
+ * they were. Sums, maxima and LSE are in 32 bits; the probabilities are rounded to
+ * dtype, fp16 ones by at most 2^-11 of themselves or 2^-32 of the row's largest.
  *
  *   shape   T, H, Hkv, d, dtype (bf16 or fp16), scale
  *   q, k, v  with strides of at least d (of 0 nowhere: give Hkv the number of

@@ -1,0 +1,122 @@
+"""The serving operators with values, scales and sizes far apart, calls repeated,
+and what they leave behind: the status word and the tensors' versions.
+
+The bounds are those of test_gpu_serving.py; what fp16 takes from small
+probabilities is bounded key by key. A probability times its value scale is held
+at 2^7 or more for the row's largest (at the running maximum, which is never above
+the final one), so rounding takes at most 2^-25 / 2^7 of the largest, or the whole
+of it: sum_j min(p_j b_j, 2^-32 max p b) |code_j|, over the keys that the row sees.
+"""
+import numpy as np
+import pytest
+import torch
+
+import attention_jvp_attn_b200 as aj
+from attention_jvp_attn_b200 import inputs as wl
+from oracle import serving_oracle as orc
+from test_gpu_serving import F8, check_attn, f64, filled, ints, ok, pool, randn, rng, same_codes, stale, tables
+
+pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
+
+
+def taken(q, cache, v_scale, lens, table, causal, scale, k_scale=None):
+    """What fp16 may take of each output: [B, n, H, d]."""
+    B, n, H, d = q.shape
+    group = H // cache.k.shape[1]
+    one = np.ones_like(v_scale)
+    out = np.zeros(q.shape)
+    kc, vc = f64(cache.k), f64(cache.v)
+    ks = f64(cache.k_scale) if k_scale is None else k_scale
+    for b, m in enumerate(lens):
+        k = orc.cache_values(kc, ks, table[b], m)
+        code = np.abs(orc.cache_values(vc, one, table[b], m))
+        size = orc.cache_values(np.ones_like(vc), v_scale, table[b], m)[..., 0]
+        for h in range(H):
+            for i in range(n):
+                seen = min(max(m - n + 1 + i, 0), m) if causal else m
+                if seen == 0:
+                    continue
+                x = scale * (k[h // group][:seen] @ f64(q[b, i, h]))
+                p = np.exp(x - x.max())
+                pb = p / p.sum() * size[h // group][:seen]
+                out[b, i, h] = np.minimum(pb, 2.0 ** -32 * pb.max()) @ code[h // group][:seen]
+    return out
+
+
+# ------------------------------------------------------------------ scales and scores far apart
+@pytest.mark.parametrize("up", [10, 20, 26])
+@pytest.mark.parametrize("length,n,H,Hkv,d,dtype,width", [
+    (500, 1, 4, 2, 64, torch.float16, 32), (500, 4, 4, 1, 128, torch.bfloat16, 32), (4900, 1, 2, 1, 128, torch.float16, 310),
+    (500, 24, 2, 2, 64, torch.float16, 32), (700, 140, 1, 1, 128, torch.float16, 48)])
+def test_one_page_of_a_large_scale(up, length, n, H, Hkv, d, dtype, width):
+    """One token of large values raises its page's scale by 2^up and gets next to no
+    probability; its page-mates hold zeros. The output is made of all other tokens."""
+    g = rng(up + length + n)
+    page = 16
+    cache = filled(g, -(-length // page) + 2, Hkv, page, d)
+    table = tables(g, cache.k.shape[0], [length], page, width)
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(2.0 ** -7)
+    cache.k.view(torch.uint8).zero_()
+    first = cache.k.view(torch.uint8)[..., 0]  # scores are s q_0 k_0, with s = q_0 = 1
+    at = table[0, 11].item()
+    first[at] = torch.tensor([0.3125], device="cuda").to(F8).view(torch.uint8)
+    first[at, :, 5] = torch.tensor([-40.0], device="cuda").to(F8).view(torch.uint8)
+    cache.v_scale[at] = 2.0 ** (up - 7)
+    cache.v.view(torch.uint8)[at] = 0
+    cache.v.view(torch.uint8)[at, :, 5] = torch.tensor([448.0], device="cuda").to(F8).view(torch.uint8)
+    q = randn(g, 1, n, H, d, dtype=dtype)
+    q[..., 0] = 1.0
+    tab = table.cpu().numpy()
+    causal = n < 140
+    ref = orc.cache_attn(f64(q), f64(cache.k), f64(cache.v), f64(cache.k_scale), f64(cache.v_scale), [length], tab, causal, 1.0)
+    lost = taken(q, cache, f64(cache.v_scale), [length], tab, causal, 1.0)
+    o, lse = aj.cache_attn(q, cache, ints([length]), table, causal=causal, scale=1.0)
+    ok()
+    check_attn(o, lse, q, ref, 1.0, 2.0 ** -11, lost)
+
+
+@pytest.mark.parametrize("n,H,d,dtype", [(1, 4, 64, torch.bfloat16), (3, 4, 128, torch.float16), (60, 4, 64, torch.float16),
+                                         (150, 2, 128, torch.bfloat16)])
+def test_scales_of_any_size_key_by_key(n, H, d, dtype):
+    """Value scales that differ by 2^20 from page to page, none a power of two."""
+    g = rng(41 + n)
+    cache = filled(g, 60, 2, 16, d)
+    for s in (cache.k_scale, cache.v_scale):
+        s.mul_(torch.exp(torch.rand(s.shape, generator=g, device="cuda")))
+    cache.v_scale.mul_(torch.exp2(torch.randint(-10, 11, (60, 2), generator=g, device="cuda").float()))
+    lens = [500, 290]
+    table = tables(g, 60, lens, 16)
+    tab = table.cpu().numpy()
+    q = randn(g, 2, n, H, d, dtype=dtype)
+    scale = 1 / np.sqrt(d)
+    ref = orc.cache_attn(f64(q), f64(cache.k), f64(cache.v), f64(cache.k_scale), f64(cache.v_scale), lens, tab, True, scale)
+    lost = taken(q, cache, f64(cache.v_scale), lens, tab, True, scale)
+    o, lse = aj.cache_attn(q, cache, ints(lens), table, scale=scale)
+    ok()
+    check_attn(o, lse, q, ref, scale, 2.0 ** -11, lost)
+
+
+@pytest.mark.parametrize("T,H,Hkv,d", [(300, 2, 1, 64), (700, 4, 2, 128), (1400, 64, 2, 64)])
+def test_prompt_behind_a_sink(T, H, Hkv, d):
+    """A first key 16 above all others in the exponent, with values of 0: fp16 must
+    keep the others' probabilities."""
+    g = rng(T)
+    q, v = randn(g, T, H, d, dtype=torch.float16), randn(g, T, Hkv, d, dtype=torch.float16)
+    k = torch.zeros(T, Hkv, d, dtype=torch.float16, device="cuda")
+    q[..., 0] = 1.0
+    k[0, :, 0] = 16.0
+    v[0] = 0.0
+    heads = slice(0, H, max(H // 4, 1))
+    ref = orc.prompt_attn(f64(q[:, heads]), f64(k).repeat(H // Hkv, 1)[:, heads], f64(v).repeat(H // Hkv, 1)[:, heads], [0, T], 1.0)
+    p = np.exp(-16.0) / (1.0 + np.arange(T) * np.exp(-16.0))  # of each other key, for row t
+    top = 1.0 / (1.0 + np.arange(T) * np.exp(-16.0))
+    sums = np.cumsum(np.abs(f64(v)), 0).repeat(H // Hkv, 1)[:, heads]
+    lost = np.minimum(p, 2.0 ** -32 * top)[:, None, None] * sums
+    o, lse = aj.prompt_attn(q, k, v, ints([0, T]), scale=1.0)
+    ok()
+    check_attn(o[:, heads], lse[heads], q, ref, 1.0, 2.0 ** -11, lost)
+
+
+# ------------------------------------------------------------------ append
