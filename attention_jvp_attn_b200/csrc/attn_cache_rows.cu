@@ -307,9 +307,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_k
       if constexpr (!std::is_same<T, __half>::value) {
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        int e = 0;
-        if (amax > 0.f) frexpf(amax, &e);
-        e = min(max(e, -100), 100);
+        const int e = query_exp(amax);
         inv = ldexpf(1.f, -e);
         mine *= ldexpf(1.f, e);
       }

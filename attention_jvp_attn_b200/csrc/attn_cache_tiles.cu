@@ -583,9 +583,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
               amax = fmaxf(amax, a < INFINITY ? a : 0.f);
             }
           }
-          int e = 0;
-          if (amax > 0.f) frexpf(amax, &e);
-          e = min(max(e, -100), 100);
+          const int e = query_exp(amax);
           inv = ldexpf(1.f, -e);
           row_scale *= ldexpf(1.f, e);
         }

@@ -34,6 +34,16 @@ __device__ __forceinline__ float read_scale(float s) {
   return fminf(fmaxf(s, kMinScale), kMaxScale);  // a NaN reads as the smallest
 }
 
+// e of the power of two 2^-e that scales a row of bf16 queries, amax the largest
+// finite |q|, into fp16: to below 1, as far as 2^e and 2^-e are normal 32-bit
+// numbers (subnormal rows have few bits anyway), and from 2^113 on only to below
+// 2^15, which keeps 2^e times the softmax scale in range.
+__device__ __forceinline__ int query_exp(float amax) {
+  int e = 0;
+  if (amax > 0.f) frexpf(amax, &e);
+  return min(max(e, -126), 113);
+}
+
 // Length of sequence b in the cache; 0 and an error if it is out of range.
 __device__ __forceinline__ int checked_len(const CacheAttnParams& p, int b) {
   const int len = p.lens[b];

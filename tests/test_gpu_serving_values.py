@@ -119,4 +119,21 @@ def test_prompt_behind_a_sink(T, H, Hkv, d):
     check_attn(o[:, heads], lse[heads], q, ref, 1.0, 2.0 ** -11, lost)
 
 
+@pytest.mark.parametrize("size", [118, 127, -118, -126])
+@pytest.mark.parametrize("n,H,d", [(1, 4, 64), (2, 8, 128), (40, 4, 128), (70, 4, 64)])
+def test_queries_of_any_size(size, n, H, d):
+    """bf16 queries at the ends of the type's range, their size taken back by the scale."""
+    g = rng(n + H)
+    cache = filled(g, 20, 2, 32, d)
+    table = tables(g, 20, [300], 32)
+    q = randn(g, 1, n, H, d).clamp(-1.5, 1.5)
+    q = (q.double() * 2.0 ** size).to(torch.bfloat16)
+    scale = 0.1 * 2.0 ** -size
+    ref = orc.cache_attn(f64(q), f64(cache.k), f64(cache.v), f64(cache.k_scale), f64(cache.v_scale), [300],
+                         table.cpu().numpy(), True, np.float64(np.float32(scale)))
+    o, lse = aj.cache_attn(q, cache, ints([300]), table, scale=scale)
+    ok()
+    check_attn(o, lse, q, ref, scale, 2.0 ** -11, 300 * 448 * 2.0 ** -7 * 2.0 ** -25)
+
+
 # ------------------------------------------------------------------ append
