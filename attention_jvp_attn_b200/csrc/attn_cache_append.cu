@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(THREADS, PER * sizeof(T) <= 4 ? 1024 / THREADS
   for (int u = 0; u < UN; ++u) {
     const int which = unit0 + u >= p.heads ? 1 : 0, head = unit0 + u - which * p.heads;
     before[u] = 0.f;
-    if (unit0 + u < units && lo > 0) before[u] = p.scale[which][page * p.scale_page + head * p.scale_head];
+    if (unit0 + u < units && lo > 0)
+      before[u] = read_scale(p.scale[which][page * p.scale_page + head * p.scale_head]);
   }
 #pragma unroll
   for (int u = 0; u < UN; ++u) {
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   if (mine) load(row0);
   if (!page_exists(p, part) || !has) return;
   float* scale = p.scale[which] + part.page * p.scale_page + head * p.scale_head;
-  const float before = part.lo > 0 ? *scale : 0.f;
+  const float before = part.lo > 0 ? read_scale(*scale) : 0.f;
   float x[16], amax = 0.f;
   if (mine) {
     value(x);

@@ -26,13 +26,7 @@ struct CacheAttnParams {
   float scale_log2;
 };
 
-constexpr float kMinScale = 9.094947017729282e-13f;  // 2^-40
-constexpr float kMaxScale = 1.099511627776e12f;      // 2^40
 constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float read_scale(float s) {
-  return fminf(fmaxf(s, kMinScale), kMaxScale);  // a NaN reads as the smallest
-}
 
 // e of the power of two 2^-e that scales a row of bf16 queries, amax the largest
 // finite |q|, into fp16: to below 1, as far as 2^e and 2^-e are normal 32-bit

@@ -211,6 +211,13 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, ui
       : "r"(codes));
 }
 
+// ---- device: page scales ----
+constexpr float kMinScale = 9.094947017729282e-13f;  // 2^-40
+constexpr float kMaxScale = 1.099511627776e12f;      // 2^40
+__device__ __forceinline__ float read_scale(float s) {
+  return fminf(fmaxf(s, kMinScale), kMaxScale);  // a NaN reads as the smallest
+}
+
 // The start of sequence b's rows in a packed array of T rows, from data that
 // may be out of order: always in [0, T], so that no row outside is touched.
 __device__ __forceinline__ int clamp_row(int start, int T) { return min(max(start, 0), T); }

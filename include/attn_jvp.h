@@ -568,10 +568,12 @@ typedef struct {
  *
  * The scale of a page and head is a power of two: the smallest 2^e with
  * |x| <= 448 * 2^e over the finite values x of the new tokens in the page,
- * -32 <= e <= 32, and not below the page's scale before the call where the
- * page keeps earlier tokens of the sequence. Where it grows, those tokens'
+ * -32 <= e <= 32, and not below the page's scale before the call (read as the
+ * attention reads it, between 2^-40 and 2^40) where the page keeps earlier
+ * tokens of the sequence. Where it grows, those tokens'
  * codes are rounded anew to it (exact but for the smallest, subnormal codes).
- * A value is rounded once, from fp32 to e4m3 (to nearest even); values beyond
+ * A value is rounded once, from fp32 to e4m3 (to nearest even; behind a scale of
+ * the caller's own that is no power of two, its quotient in fp32 is); values beyond
  * 448 * 2^e, infinities among them, become the largest code, NaN stays NaN.
  * Rows of a page behind the last appended token are left as they were. Calling
  * it twice with the same arguments gives the same cache.

@@ -136,4 +136,48 @@ def test_queries_of_any_size(size, n, H, d):
     check_attn(o, lse, q, ref, scale, 2.0 ** -11, 300 * 448 * 2.0 ** -7 * 2.0 ** -25)
 
 
+@pytest.mark.parametrize("n,H", [(1, 4), (6, 4), (40, 4)])
+def test_scales_that_are_none(n, H):
+    """Page scales of 0, below 0, NaN, infinite, too small and too large are read as
+    the limits that they pass (a NaN as the smallest)."""
+    g = rng(n)
+    cache = filled(g, 30, 2, 16, 64)
+    lens = [300, 130]
+    table = tables(g, 30, lens, 16)
+    for i, s in enumerate((0.0, -1.0, NAN, 2.0 ** -60, -INF)):
+        cache.k_scale[table[0, 2 + i].item()] = s
+        cache.v_scale[table[1, 1 + i].item()] = s
+    cache.v_scale[table[0, 3].item(), 0] = INF
+    cache.v_scale[table[0, 4].item(), 1] = 2.0 ** 50
+    clamp = lambda t: np.where(np.isnan(f64(t)), 2.0 ** -40, np.clip(f64(t), 2.0 ** -40, 2.0 ** 40))
+    ks, vs, tab = clamp(cache.k_scale), clamp(cache.v_scale), table.cpu().numpy()
+    q = randn(g, 2, n, H, 64)
+    ref = orc.cache_attn(f64(q), f64(cache.k), f64(cache.v), ks, vs, lens, tab, True, 0.125)
+    lost = taken(q, cache, vs, lens, tab, True, 0.125, ks)
+    o, lse = aj.cache_attn(q, cache, ints(lens), table)
+    ok()
+    check_attn(o, lse, q, ref, 0.125, 2.0 ** -11, lost)
+
+
 # ------------------------------------------------------------------ append
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("before,read", [(0.0, 2.0 ** -40), (-1.0, 2.0 ** -40), (NAN, 2.0 ** -40), (-INF, 2.0 ** -40),
+                                         (2.0 ** -60, 2.0 ** -40), (2.0 ** 50, 2.0 ** 40), (INF, 2.0 ** 40)])
+def test_append_behind_a_scale_that_is_none(new, before, read):
+    """The scale of a page that keeps earlier tokens counts as the attention reads it."""
+    g = rng(9)
+    cache = filled(g, 4, 2, 64, 64)
+    cache.k_scale[1], cache.v_scale[1] = before, before
+    k, v = randn(g, new, 2, 64), randn(g, new, 2, 64, size=2.0 ** -30)
+    scales = [f64(s).copy() for s in (cache.k_scale, cache.v_scale)]
+    for s in scales:
+        s[1] = read
+    want_k = orc.append(f64(cache.k), scales[0], f64(k), [0, new], [11], [[1]])
+    want_v = orc.append(f64(cache.v), scales[1], f64(v), [0, new], [11], [[1]])
+    aj.cache_append(cache, k, v, ints([0, new]), ints([11]), ints([[1]]))
+    ok()
+    assert (f64(cache.k_scale) == want_k[1]).all() and (f64(cache.v_scale) == want_v[1]).all()
+    same_codes(cache.k, want_k[0])
+    same_codes(cache.v, want_v[0])
