@@ -260,7 +260,8 @@ def attn_jvp_host(q, k, v, tq, tk, tv, mode: int, chunk_tokens: int, n_chunks: i
 
 def sync_status(device: Optional[torch.device] = None) -> int:
     """Synchronize the current stream and return (and clear) the library's
-    device status (0 = ok, 5 = a kernel's bounded wait ran out)."""
+    device status (0 = ok, 5 = a kernel's bounded wait ran out, 7 = a serving
+    operator met a position, length or page out of range)."""
     dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(dev):
         return int(_abi.load().attn_jvp_sync_status(_stream_handle(dev)))

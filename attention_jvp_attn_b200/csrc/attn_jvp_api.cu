@@ -29,7 +29,7 @@ struct DeviceState {
   int status_code = ATTN_JVP_OK;  // why the device is unusable, if it is
   int sm_count = 0;
   int pair_clusters = 0;           // CTA pairs resident at once (0: pair kernel unavailable)
-  unsigned int* status = nullptr;  // device status word (bit 0: a bounded wait ran out)
+  unsigned int* status = nullptr;  // device status word (bit 0: a bounded wait ran out, bit 1: a bad index)
   // Grid-barrier words of the fused rotary-embedding launches (kGridSlots of
   // them after the status word, in the same allocation), and the launch count
   // that tags them.
@@ -107,6 +107,28 @@ int device_state(DeviceState** out) {
   }
   *out = &st;
   return ATTN_JVP_OK;
+}
+
+// Synchronizes `stream`, then reports and clears the bits of the device status
+// word that are in `which`.
+int read_status(void* stream, unsigned int which) {
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc != ATTN_JVP_OK) return rc;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_JVP_ERR_CUDA;
+  }
+  unsigned int word = 0;
+  if (cudaMemcpy(&word, st->status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_JVP_ERR_CUDA;
+  }
+  if ((word & which) == 0) return ATTN_JVP_OK;
+  const unsigned int rest = word & ~which;
+  cudaMemcpy(st->status, &rest, sizeof(rest), cudaMemcpyHostToDevice);
+  // a wait that ran out outweighs a bad index: it invalidates more
+  return (word & which & ajvp::kStatusTimeout) ? ATTN_JVP_ERR_DEVICE_TIMEOUT : ATTN_JVP_ERR_BAD_INDEX;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -744,29 +766,11 @@ int attn_jvp_fwd_host(const attn_jvp_shape* shape, const void* h_q, const void* 
     cudaGetLastError();
     return ATTN_JVP_ERR_CUDA;
   }
-  return attn_jvp_sync_status(stream);
+  // a bad index is another call's: it stays for attn_jvp_sync_status
+  return read_status(stream, ajvp::kStatusTimeout);
 }
 
-int attn_jvp_sync_status(void* stream) {
-  DeviceState* st = nullptr;
-  int rc = device_state(&st);
-  if (rc != ATTN_JVP_OK) return rc;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) {
-    cudaGetLastError();
-    return ATTN_JVP_ERR_CUDA;
-  }
-  unsigned int word = 0;
-  if (cudaMemcpy(&word, st->status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) {
-    cudaGetLastError();
-    return ATTN_JVP_ERR_CUDA;
-  }
-  if (word != 0) {
-    cudaMemset(st->status, 0, sizeof(unsigned int));
-    // a wait that ran out outweighs a bad index: it invalidates more
-    return (word & ajvp::kStatusTimeout) ? ATTN_JVP_ERR_DEVICE_TIMEOUT : ATTN_JVP_ERR_BAD_INDEX;
-  }
-  return ATTN_JVP_OK;
-}
+int attn_jvp_sync_status(void* stream) { return read_status(stream, ~0u); }
 
 const char* attn_jvp_status_string(int status) {
   switch (status) {

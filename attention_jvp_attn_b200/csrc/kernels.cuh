@@ -101,7 +101,7 @@ bool bwd_tc_supported(int64_t B, int64_t L, int64_t H, int64_t d);
 int bwd_tc_launch(const BwdTcArgs& a, cudaStream_t stream);  // ATTN_JVP_* status
 
 // ---- services of the C ABI layer for the other kernel files ----
-// The current device's status word (bit 0: a bounded wait ran out), set up
+// The current device's status word (bit 0: a bounded wait ran out, bit 1: a bad index), set up
 // once per device; returns an ATTN_JVP_* status.
 int device_status_word(unsigned int** word);
 // The same, and the device's number of SMs.

@@ -202,8 +202,10 @@ int64_t attn_jvp_host_staging_bytes(const attn_jvp_shape* shape);
 /*
  * attn_jvp_sync_status - synchronizes `stream`, then reports and clears the
  * device status word of the current device: ATTN_JVP_ERR_DEVICE_TIMEOUT if a
- * kernel gave up on a bounded wait since the last call, ATTN_JVP_ERR_CUDA if
- * the stream reported an error, else ATTN_JVP_OK.
+ * kernel gave up on a bounded wait since the last call, else
+ * ATTN_JVP_ERR_BAD_INDEX if a serving operator met a position, length or page out
+ * of range (attn_jvp_fwd_host, which reports the first, leaves the second),
+ * ATTN_JVP_ERR_CUDA if the stream reported an error, else ATTN_JVP_OK.
  */
 int attn_jvp_sync_status(void* stream);
 

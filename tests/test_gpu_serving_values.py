@@ -181,3 +181,18 @@ def test_append_behind_a_scale_that_is_none(new, before, read):
     assert (f64(cache.k_scale) == want_k[1]).all() and (f64(cache.v_scale) == want_v[1]).all()
     same_codes(cache.k, want_k[0])
     same_codes(cache.v, want_v[0])
+
+
+# ------------------------------------------------------------------ what a call leaves behind
+def test_bad_index_does_not_fail_the_host_call():
+    """A serving call's bad index is not an error of attn_jvp_host, and is reported after it."""
+    w = wl.Workload("host_small", B=1, H=2, d=64, n_chunks=2, chunk_tokens=20, mode=wl.TEACHER_FORCING, seed=3)
+    host = {n: t.cpu().pin_memory() for n, t in wl.make_inputs(w, device="cuda").items()}
+    outs = [torch.empty_like(host["q"]).pin_memory() for _ in range(2)]
+    lse = torch.empty(1, 2, host["q"].shape[1], dtype=torch.float32).pin_memory()
+    cos, sin = aj.rope_tables(64, 8)
+    aj.rope_at(randn(rng(1), 2, 1, 64), None, torch.tensor([3, 99], device="cuda"), cos, sin)
+    staging = torch.empty(aj.host_staging_bytes(1, host["q"].shape[1], 2, 64, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    aj.attn_jvp_host(*(host[n] for n in ("q", "k", "v", "tq", "tk", "tv")), w.mode, w.chunk_tokens, w.n_chunks, staging,
+                     (*outs, lse))
+    assert aj.sync_status() == 7 and aj.sync_status() == 0
