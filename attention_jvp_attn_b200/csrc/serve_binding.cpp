@@ -182,6 +182,12 @@ void call(const char* name, c10::Device device, F f) {
   }
 }
 
+// A tensor of the caller's was written over: autograd, which may have saved it,
+// goes by its version (inference tensors have none).
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // rope_at(q, k, positions, cos, sin, layout, transpose, out)
 PyObject* rope_at(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -221,6 +227,8 @@ PyObject* rope_at(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(qo.sizes() == q.sizes() && !k == !ko && (!k || ko->sizes() == k->sizes()),
                     "out must give tensors of q's and k's shapes");
   run(qo, rows(qo, "out", &q), ko, ko ? rows(*ko, "out", &q) : attn_jvp_strides{0, 0});
+  written(qo);
+  if (ko) written(*ko);
   return given(out.a, out.b);
   END_HANDLE_TH_ERRORS
 }
@@ -253,6 +261,7 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           static_cast<const int32_t*>(table.data_ptr()), table.size(1), table.stride(0),
                           turn ? &tables : nullptr, stream);
   });
+  for (const Tensor* t : {cache.k, cache.v, cache.k_scale, cache.v_scale}) written(*t);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -312,6 +321,8 @@ PyObject* cache_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor &o = tensor(out.a, "out"), &lse = tensor(out.b, "out");
   check_out(o, lse, q, {B, H, L});
   run(o, lse);
+  written(o);
+  written(lse);
   return given(out.a, out.b);
   END_HANDLE_TH_ERRORS
 }
@@ -346,6 +357,8 @@ PyObject* prompt_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor &o = tensor(out.a, "out"), &lse = tensor(out.b, "out");
   check_out(o, lse, q, {H, T});
   run(o, lse);
+  written(o);
+  written(lse);
   return given(out.a, out.b);
   END_HANDLE_TH_ERRORS
 }

@@ -196,3 +196,37 @@ def test_bad_index_does_not_fail_the_host_call():
     aj.attn_jvp_host(*(host[n] for n in ("q", "k", "v", "tq", "tk", "tv")), w.mode, w.chunk_tokens, w.n_chunks, staging,
                      (*outs, lse))
     assert aj.sync_status() == 7 and aj.sync_status() == 0
+
+
+def test_written_tensors_get_a_new_version():
+    """Autograd notices that a tensor which it saved was written over."""
+    g = rng(2)
+    q, k = randn(g, 4, 2, 64), randn(g, 4, 1, 64)
+    cos, sin = aj.rope_tables(64, 8)
+    pos, starts = ints([0, 1, 2, 3]), ints([0, 4])
+
+    def raised(call, *written, kept=()):
+        before = [t._version for t in (*written, *kept)]
+        call()
+        after = [t._version for t in (*written, *kept)]
+        assert all(a > b for a, b in zip(after[:len(written)], before))
+        assert after[len(written):] == before[len(written):]
+
+    raised(lambda: aj.rope_at(q, k, pos, cos, sin, out=(q, k)), q, k, kept=(cos, sin, pos))
+    raised(lambda: aj.rope_at(q, None, pos, cos, sin, out=(q, None)), q)
+    cache = aj.paged_cache(2, 16, 1, 64)
+    raised(lambda: aj.cache_append(cache, k, k, starts, ints([0]), ints([[1]])), *cache, kept=(k,))
+    out = aj.prompt_attn(q, k, k, starts)
+    raised(lambda: aj.prompt_attn(q, k, k, starts, out=out), *out, kept=(q, k))
+    out = aj.cache_attn(q[None], cache, ints([4]), ints([[1]]))
+    raised(lambda: aj.cache_attn(q[None], cache, ints([4]), ints([[1]]), out=out), *out, kept=(q, *cache))
+    with torch.inference_mode():  # tensors without versions
+        x = q.clone()
+        aj.rope_at(x, None, pos, cos, sin, out=(x, None))
+    ok()
+    w = torch.ones(4, 2, 64, device="cuda", requires_grad=True)
+    y = q.float()
+    loss = (w * y).sum()
+    aj.rope_at(y, None, pos, cos, sin, out=(y, None))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
