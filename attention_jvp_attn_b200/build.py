@@ -1,8 +1,11 @@
-"""Build the CUDA library libattn_jvp.so in-tree for sm_100a with nvcc, and the
+"""Build the CUDA library libattn_jvp.so in-tree for sm_100a with nvcc, and then the
 Python binding of the serving operators, _serving.so, with the C++ compiler.
 
     python -m attention_jvp_attn_b200.build [--force] [--verbose]
 
+The library needs nvcc only. The binding also needs torch's and Python's headers and
+g++; where one is missing it is left out, with a message, and the serving operators
+say so when they are called from Python.
 The library is a plain shared object with a C ABI (include/attn_jvp.h); the
 CUDA runtime is linked statically, and the driver entry point for tensor-map
 encoding is resolved at run time, so loading it needs no GPU.
@@ -10,6 +13,7 @@ encoding is resolved at run time, so loading it needs no GPU.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -24,6 +28,8 @@ LIB = os.path.join(PKG, "libattn_jvp.so")
 BINDING = os.path.join(PKG, "_serving.so")
 # Opt-in variant whose bf16 kernel records per-tile event clocks of CTA 0.
 TRACE_LIB = os.path.join(PKG, "libattn_jvp_trace.so")
+
+BINDING_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -59,21 +65,39 @@ def _run(cmd, verbose: bool):
     return res.stdout + res.stderr
 
 
+def binding_built_for() -> str:
+    """What a binding must have been built for: it reads the tensors of one torch, in
+    the Python of one ABI. The binding holds this text as `built_for`."""
+    import torch
+    return (f"torch {torch.__version__} abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} python "
+            f"{sysconfig.get_config_var('EXT_SUFFIX')} flags {' '.join(BINDING_FLAGS)}")
+
+
+def binding_lacks():
+    """What is missing here to build the binding."""
+    have = {"torch": importlib.util.find_spec("torch"), "g++": shutil.which("g++"),
+            "Python.h": os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))}
+    return [name for name, found in have.items() if not found]
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """_serving.so: it reads torch tensors, so it is built against this torch,
     and by the g++ that nvcc takes too: one with a C++ runtime of its own linked
     in statically crashes beside torch's as soon as a message formats a number."""
     src, header = os.path.join(CSRC, "serve_binding.cpp"), os.path.join(INCLUDE, "attn_jvp.h")
+    key = binding_built_for()
     if not force and os.path.exists(BINDING) and \
             all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in (src, header)):
-        return BINDING
+        with open(BINDING, "rb") as f:
+            if key.encode() + b"\0" in f.read():
+                return BINDING
     import torch
     at = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     includes = [INCLUDE, os.path.join(at, "include"), os.path.join(at, "include/torch/csrc/api/include"),
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    out = _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+    out = _run([shutil.which("g++"), *BINDING_FLAGS,
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DAJVP_BUILT_FOR="{key}"',
                 *(f for i in includes for f in ("-isystem", i)), "-o", BINDING + ".tmp", src,
                 "-L" + os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], verbose)
     if verbose:
@@ -84,8 +108,18 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
           trace: bool = False) -> str:
+    lib = build_library(force, verbose, ptxas_info, trace)
     if not trace:
-        build_binding(force, verbose)
+        lacks = binding_lacks()
+        if lacks:
+            print(f"serving binding not built: no {' and no '.join(lacks)} here", file=sys.stderr)
+        else:
+            build_binding(force, verbose)
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
+                  trace: bool = False) -> str:
     lib = TRACE_LIB if trace else LIB
     if not force and up_to_date(lib):
         return lib

@@ -389,4 +389,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__serving() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__serving() {
+  PyObject* m = PyModule_Create(&module);
+  // the torch and the Python that this was compiled against (build.py)
+  if (m && PyModule_AddStringConstant(m, "built_for", AJVP_BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -43,10 +43,13 @@ def _native():
     if _bound is None or _bound[0] is not lib:
         with _lock:
             try:
-                from . import _serving
+                from . import _serving, build
             except ImportError as e:
                 raise RuntimeError("binding of the serving operators not built or not loadable "
                                    f"(run `python -m attention_jvp_attn_b200.build`): {e}") from e
+            if _serving.built_for != build.binding_built_for():
+                raise RuntimeError(f"binding of the serving operators built for {_serving.built_for!r}, this is "
+                                   f"{build.binding_built_for()!r} (run `python -m attention_jvp_attn_b200.build`)")
             _serving.bind(_abi.check, *(_abi.address(lib, f) for f in (
                 "attn_jvp_rope_at", "attn_jvp_cache_append", "attn_jvp_cache_attn",
                 "attn_jvp_cache_attn_workspace_bytes", "attn_jvp_prompt_attn")))
