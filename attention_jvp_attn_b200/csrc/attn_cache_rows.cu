@@ -816,7 +816,7 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
   const attn_jvp_shape& s = *shape;
   int rc = check_attn_shape(s, Hkv);
   if (rc != ATTN_JVP_OK) return rc;
-  if (max_len < 0 || !(s.scale <= 0.f || std::isfinite(s.scale))) return ATTN_JVP_ERR_INVALID_ARGUMENT;
+  if (max_len < 0 || !good_scale(s.scale)) return ATTN_JVP_ERR_INVALID_ARGUMENT;
   if ((rc = check_cache(cache, Hkv, s.d)) != ATTN_JVP_OK) return rc;
   if (table_width < 1 || table_width > (int64_t(1) << 30) / cache->page_tokens ||
       (s.B > 1 && table_stride < table_width))
@@ -849,8 +849,7 @@ extern "C" int attn_jvp_cache_attn(const attn_jvp_shape* shape, int64_t Hkv, con
   p.page_shift = 4;
   while ((1 << p.page_shift) < cache->page_tokens) ++p.page_shift;
   p.causal = causal != 0;
-  const float scale = s.scale > 0.f ? s.scale : 1.0f / std::sqrt(static_cast<float>(s.d));
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2(s.scale, s.d);
   const int64_t bound = table_width * cache->page_tokens;
   const int64_t len = max_len > 0 && max_len < bound ? max_len : bound;
   const int64_t rows = s.L * p.group;

@@ -519,7 +519,7 @@ extern "C" int attn_jvp_prompt_attn(const attn_jvp_tokens* shape, const void* q,
   if ((s.dtype != ATTN_JVP_BF16 && s.dtype != ATTN_JVP_F16) || (s.d != 64 && s.d != 128))
     return ATTN_JVP_ERR_UNSUPPORTED;
   if (s.T < 0 || s.T > (int64_t(1) << 30) || s.H < 1 || s.H > 65535 || s.Hkv < 1 || s.H % s.Hkv ||
-      B < 0 || B > (1 << 20) || !(s.scale <= 0.f || std::isfinite(s.scale)))
+      B < 0 || B > (1 << 20) || !good_scale(s.scale))
     return ATTN_JVP_ERR_INVALID_ARGUMENT;
   if (s.T == 0 || B == 0) return ATTN_JVP_OK;
   if (!starts || !o || !lse) return ATTN_JVP_ERR_INVALID_ARGUMENT;
@@ -553,8 +553,7 @@ extern "C" int attn_jvp_prompt_attn(const attn_jvp_tokens* shape, const void* q,
   const bool single = pieces * s.H <= sms;
   if (single) pieces = s.T / kTile + B;
   p.pieces = static_cast<int>(pieces);
-  const float scale = s.scale > 0.f ? s.scale : 1.0f / std::sqrt(static_cast<float>(s.d));
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2(s.scale, s.d);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   auto launch = [&](auto one) {

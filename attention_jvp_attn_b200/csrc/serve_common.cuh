@@ -24,6 +24,13 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// A softmax scale (<= 0: the default), which the kernels take times log2 e.
+constexpr float kLog2e = 1.4426950408889634f;
+inline bool good_scale(float s) { return s <= 0.f || std::isfinite(s * kLog2e); }
+inline float scale_log2(float s, int64_t d) {
+  return (s > 0.f ? s : 1.0f / std::sqrt(static_cast<float>(d))) * kLog2e;
+}
+
 inline int dtype_bytes(int32_t dtype) {
   return dtype == ATTN_JVP_F32 ? 4 : (dtype == ATTN_JVP_BF16 || dtype == ATTN_JVP_F16) ? 2 : 0;
 }

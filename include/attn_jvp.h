@@ -501,7 +501,7 @@ typedef struct {
   int64_t Hkv;   /* key/value heads >= 1; H is a multiple of it */
   int64_t d;     /* head dim: 64 or 128 */
   int32_t dtype; /* attn_jvp_dtype */
-  float scale;   /* softmax scale s; <= 0 selects 1/sqrt(d) (attention only) */
+  float scale;   /* softmax scale s < 2.35e38; <= 0 selects 1/sqrt(d) (attention only) */
 } attn_jvp_tokens;
 
 /* Strides of a [T, heads, d] array, in elements. */
@@ -603,7 +603,7 @@ int attn_jvp_cache_append(const attn_jvp_tokens* shape, const void* k, attn_jvp_
  * i of n (causal != 0: the n queries are the sequence's last n tokens). A row
  * that sees no key gets O = 0, LSE = -infinity.
  *
- *   shape   B = sequences <= 65535, L = n <= 2^24, H, d, dtype (bf16 or fp16), scale
+ *   shape   B = sequences <= 65535, L = n <= 2^24, H, d, dtype (bf16 or fp16), scale < 2.35e38
  *   Hkv     key/value heads
  *   q       [B, n, H, d]: q_strides[0..2] in elements for B, n, H
  *   lens    [B] int32, tokens of each sequence in the cache, the new ones
