@@ -376,6 +376,7 @@ extern "C" int attn_jvp_cache_append(const attn_jvp_tokens* shape, const void* k
   if ((rc = check_rows(k, k_strides, s.T, s.Hkv, bytes)) != ATTN_JVP_OK ||
       (rc = check_rows(v, v_strides, s.T, s.Hkv, bytes)) != ATTN_JVP_OK)
     return rc;
+  if (!writable(*cache, s.Hkv, s.d)) return ATTN_JVP_ERR_INVALID_ARGUMENT;
   AppendParams p;
   rc = ajvp::device_status_word(&p.status);
   if (rc != ATTN_JVP_OK) return rc;

@@ -7,6 +7,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <array>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -102,6 +104,28 @@ inline int check_cache(const attn_jvp_cache* c, int64_t Hkv, int64_t d) {
 // bits between 1 and 65,504 would lie idle and 2^-25 of the largest be lost.
 constexpr float kLead = 7.f;
 constexpr float kRaise = 15.f;
+
+// Whether the elements of an array of `inner` adjacent ones, n[i] of them `stride[i]`
+// apart in each of three dimensions, lie apart: each dimension steps over all that
+// those of smaller strides span.
+inline bool lie_apart(int64_t inner, std::array<int64_t, 3> n, std::array<int64_t, 3> stride) {
+  std::array<int, 3> order = {0, 1, 2};
+  std::sort(order.begin(), order.end(), [&](int a, int b) { return stride[a] < stride[b]; });
+  __int128 span = inner;
+  for (const int i : order) {
+    if (n[i] <= 1) continue;
+    if (stride[i] < span) return false;
+    span += static_cast<__int128>(n[i] - 1) * stride[i];
+  }
+  return true;
+}
+
+// A cache that is written: no code or scale is another one's too.
+inline bool writable(const attn_jvp_cache& c, int64_t Hkv, int64_t d) {
+  return c.k != c.v && c.k_scale != c.v_scale &&
+         lie_apart(d, {c.pages, Hkv, c.page_tokens}, {c.page_stride, c.head_stride, c.token_stride}) &&
+         lie_apart(1, {c.pages, Hkv, 1}, {c.scale_page_stride, c.scale_head_stride, 0});
+}
 
 // Raises a kernel's shared-memory limit once per device (`done`: devices that
 // have it; the kernel's own).

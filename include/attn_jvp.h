@@ -585,8 +585,10 @@ typedef struct {
  *   starts   [B + 1] int32, non-decreasing, starts[0] >= 0, starts[B] <= T;
  *            rows outside them are ignored
  *   cached   [B] int32, tokens of each sequence in the cache before the call
+ *   cache    its pages, heads and tokens (and its scales) nested in any order:
+ *            each stride covers all that smaller ones span
  *   table    [B, table_width] int32 page numbers, table_stride apart; the pages
- *            written belong to one sequence each
+ *            written belong to one sequence each, once
  *   rope     NULL for no rotation; else n_positions must exceed every p
  */
 int attn_jvp_cache_append(const attn_jvp_tokens* shape, const void* k, attn_jvp_strides k_strides,
