@@ -23,9 +23,6 @@ DTYPE_BF16 = 0
 DTYPE_F32 = 1
 DTYPE_F16 = 2  # the serving operators only
 
-ROPE_INTERLEAVED = 0
-ROPE_HALF = 1
-
 
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("L", ctypes.c_int64), ("H", ctypes.c_int64),
@@ -41,9 +38,11 @@ class Strides(ctypes.Structure):
     _fields_ = [("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
-# The other structs of the serving operators, as bytes: shape (B, L, H, d, dtype, scale) and tokens (T, H, Hkv, d, dtype, scale),
-# rope_tables (cos, sin, n_positions, rot, layout), cache (k, v, k_scale,
-# v_scale, pages, page_tokens, three strides, two scale strides).
+# The other structs of the serving operators, as bytes, for callers of the C ABI
+# through ctypes (the package itself calls it through its C++ binding): shape (B, L, H,
+# d, dtype, scale) and tokens (T, H, Hkv, d, dtype, scale), rope_tables (cos, sin,
+# n_positions, rot, layout), cache (k, v, k_scale, v_scale, pages, page_tokens, three
+# strides, two scale strides).
 pack_shape = pack_tokens = struct.Struct("@4qif").pack
 pack_rope_tables = struct.Struct("@QQqqi4x").pack
 pack_cache = struct.Struct("@4Q7q").pack

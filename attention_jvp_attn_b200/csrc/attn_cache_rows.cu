@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) cache_rows_k
     __syncwarp();
     for (int s = s_begin + warp; s < s_end; s += kRowsWarps) {
       if (late >= 0) keep_scales(late, pending);
-      // the next stage's reads are over since the end of the last round
+      // The next stage's reads are over since the end of the last round: the matrix
+      // instructions, which the whole warp issues, have taken all that was read.
       late = next < s_end ? issued % C::STAGES : -1;
       pending = fetch(next, page);
       next += kRowsWarps;

@@ -539,9 +539,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) cache_tiles_kernel(const __g
         fence_proxy_async_shared();
         __syncwarp();
         mbar_arrive_if(&full[slot], lane == 0);
-        // The stage is given back only here, where its codes have been stored: the
-        // assembler may move reads that nothing has used yet behind the arrival
-        // and the wait for the slot, and then they see the next copy.
+        // The stage is given back only here, behind the stores that need its codes
+        // and behind the proxy fence. The stores make sure that every lane's reads
+        // are over: given back right after the reads, they were seen to return the
+        // next copy's codes (nothing had used them yet). The fence orders this warp's
+        // own stores into the stage (hidden tokens, above) before that copy.
         mbar_arrive_if(&raw_empty[st], lane == 0);
       }
       __syncwarp();

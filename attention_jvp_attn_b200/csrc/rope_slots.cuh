@@ -23,12 +23,6 @@ struct RopeSlot {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void load_slot(const T* row, const RopeSlot& sl, float (&a)[8], float (&b)[8]) {
-  load8(row + sl.c0, a);
-  load8(row + sl.c1, b);
-}
-
 // The slot's cosines and sines from a row [half] of the tables.
 __device__ __forceinline__ void load_turn(const float* cos, const float* sin, int64_t row, int half,
                                           const RopeSlot& sl, float (&c)[8], float (&s)[8]) {

@@ -181,8 +181,8 @@ __device__ __forceinline__ uint32_t went_on(const Piece* pieces, int blocks, int
 }
 
 constexpr int kRowsTile = 16;  // most query rows per key head of attn_cache_rows.cu
-// attn_cache_tiles.cu: pairs of tiles of 128 query rows on tcgen05, on at most
-// tiles_blocks(sms) blocks; `work` has tiles_work_bytes of each.
+// attn_cache_tiles.cu: pairs of tiles of 128 query rows on tcgen05, on `blocks`
+// blocks; `work` has tiles_work_bytes of each.
 cudaError_t cache_tiles_launch(const CacheAttnParams& p, int d, int dtype, int blocks, float* work,
                                cudaStream_t st);
 int64_t tiles_work_bytes(int64_t d);
