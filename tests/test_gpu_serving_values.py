@@ -159,7 +159,92 @@ def test_scales_that_are_none(n, H):
     check_attn(o, lse, q, ref, 0.125, 2.0 ** -11, lost)
 
 
+def test_tiles_of_large_pages_in_many_pieces():
+    """Pages of 128 tokens at d = 64 where the key tiles are shared out over all SMs."""
+    g = rng(77)
+    lens, n, H, Hkv = [9000, 150, 5000], 200, 4, 2
+    pages = sum(-(-m // 128) for m in lens) + 2
+    cache = filled(g, pages, Hkv, 128, 64)
+    table = tables(g, pages, lens, 128)
+    stale(cache, table, lens, 128)
+    q = randn(g, 3, n, H, 64)
+    at = [0, 1, 7, 100, 199]
+    for causal in (True, False):
+        o, lse = aj.cache_attn(q, cache, ints(lens), table, causal=causal, scale=0.1)
+        ok()
+        for b, m in enumerate(lens):
+            k, v = (orc.cache_values(f64(c), f64(s), table[b].cpu().numpy(), m)
+                    for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+            seen = np.array([max(m - n + 1 + i, 0) if causal else m for i in at])
+            r = [orc.softmax_rows(f64(q[b, at, h]), k[h // 2], v[h // 2], 0.1, seen) for h in range(H)]
+            ref = [np.stack([x[i] for x in r], 1 if r[0][i].ndim == 2 else 0) for i in range(5)]
+            lost = m * 448 * 2.0 ** -7 * 2.0 ** -32 * ref[4].T[..., None]  # equal scales but for 2^2
+            check_attn(o[b, at], lse[b][:, at], q[b], ref, 0.1, 2.0 ** -11, 4 * lost)
+
+
+# ------------------------------------------------------------------ calls repeated
+REPEATS = [  # (sequences, n, H, Hkv, d, dtype, shortest length)
+    (2, 1, 4, 4, 64, torch.bfloat16, 300),     # 1 row, clusters
+    (18, 1, 16, 2, 128, torch.float16, 200),   # 8 rows, clusters
+    (9, 4, 8, 2, 64, torch.bfloat16, 200),     # 16 rows, clusters
+    (3, 1, 2, 2, 128, torch.bfloat16, 4200),   # the same, the steps shared out
+    (20, 1, 16, 2, 64, torch.float16, 2000),
+    (5, 2, 16, 2, 128, torch.float16, 4200),
+    (27, 21, 2, 1, 64, torch.float16, 900),    # one row tile
+    (10, 60, 4, 2, 64, torch.bfloat16, 900),
+    (10, 60, 4, 2, 128, torch.bfloat16, 900),
+    (7, 130, 2, 2, 64, torch.float16, 900),    # two row tiles
+    (7, 70, 4, 2, 128, torch.bfloat16, 900),
+]
+
+
+@pytest.mark.parametrize("seqs,n,H,Hkv,d,dtype,shortest", REPEATS)
+def test_cache_attn_repeats_and_is_right(seqs, n, H, Hkv, d, dtype, shortest):
+    """The first call against the oracle (some rows), then each of many calls against it."""
+    g = rng(seqs + n)
+    lens = [shortest + 131 * b for b in range(seqs)]
+    pages = sum(-(-m // 32) for m in lens) + 2
+    cache = filled(g, pages, Hkv, 32, d)
+    table = tables(g, pages, lens, 32)
+    q = randn(g, seqs, n, H, d, dtype=dtype)
+    first = aj.cache_attn(q, cache, ints(lens), table, scale=0.05)
+    ok()
+    rows = sorted({0, n // 2, n - 1})
+    for b in sorted({0, seqs // 2, seqs - 1}):
+        m = lens[b]
+        k, v = (orc.cache_values(f64(c), f64(s), table[b].cpu().numpy(), m)
+                for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+        seen = np.array([m - n + 1 + i for i in rows])
+        r = [orc.softmax_rows(f64(q[b, rows, h]), k[h * Hkv // H], v[h * Hkv // H], 0.05, seen) for h in range(H)]
+        ref = [np.stack([x[i] for x in r], 1 if r[0][i].ndim == 2 else 0) for i in range(5)]
+        lost = 4 * m * 448 * 2.0 ** -7 * 2.0 ** -32 * ref[4].T[..., None]
+        check_attn(first[0][b, rows], first[1][b][:, rows], q[b], ref, 0.05, 2.0 ** -11, lost)
+    for _ in range(50):
+        o, lse = aj.cache_attn(q, cache, ints(lens), table, scale=0.05)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    ok()
+
+
 # ------------------------------------------------------------------ append
+def test_append_of_a_skewed_batch():
+    """One long sequence among a thousand single tokens: the mean is below five."""
+    g = rng(55)
+    new, page, heads, d = [1] * 500 + [3000] + [1] * 523, 128, 2, 128
+    cached = [(i * 37) % 300 for i in range(1024)]
+    lens = [a + b for a, b in zip(new, cached)]
+    pages = sum(-(-n // page) for n in lens) + 2
+    cache = pool(g, pages, heads, page, d)
+    table = tables(g, pages, lens, page)
+    starts = np.concatenate([[0], np.cumsum(new)])
+    kv = randn(g, int(starts[-1]), 2 * heads, d, size=3.0)
+    k, v = kv[:, :heads], kv[:, heads:]
+    want_k = orc.append(f64(cache.k), f64(cache.k_scale), f64(k), starts, cached, table.cpu().numpy())
+    want_v = orc.append(f64(cache.v), f64(cache.v_scale), f64(v), starts, cached, table.cpu().numpy())
+    aj.cache_append(cache, k, v, ints(starts), ints(cached), table)
+    ok()
+    assert (f64(cache.k_scale) == want_k[1]).all() and (f64(cache.v_scale) == want_v[1]).all()
+    same_codes(cache.k, want_k[0])
+    same_codes(cache.v, want_v[0])
 
 
 @pytest.mark.parametrize("new", [1, 40])
