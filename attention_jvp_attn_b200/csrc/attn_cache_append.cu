@@ -111,8 +111,11 @@ __device__ __forceinline__ float max_finite(const float* x, int n) {  // a NaN i
 }
 
 // A page's scale for new values up to amax, `before` being its scale where it
-// keeps earlier tokens (else 0), and the scale's inverse.
-__device__ __forceinline__ void page_scale(float amax, float before, float& after, float& inv) {
+// `keeps` earlier tokens, and the scale's inverse. `before` becomes what it counts
+// as (0 without such tokens), only here: looked at where it is loaded, it would be
+// waited for there, 0.2 us before the maximum is found.
+__device__ __forceinline__ void page_scale(float amax, bool keeps, float& before, float& after, float& inv) {
+  before = keeps ? read_scale(before) : 0.f;
   // amax = f 2^E with 1 <= f < 2, and 448 = 1.75 * 2^8 (a subnormal amax is
   // below the smallest scale anyway)
   const uint32_t bits = __float_as_uint(amax);
@@ -187,8 +190,7 @@ __global__ void __launch_bounds__(THREADS, PER * sizeof(T) <= 4 ? 1024 / THREADS
   for (int u = 0; u < UN; ++u) {
     const int which = unit0 + u >= p.heads ? 1 : 0, head = unit0 + u - which * p.heads;
     before[u] = 0.f;
-    if (unit0 + u < units && lo > 0)
-      before[u] = read_scale(p.scale[which][page * p.scale_page + head * p.scale_head]);
+    if (unit0 + u < units && lo > 0) before[u] = p.scale[which][page * p.scale_page + head * p.scale_head];
   }
 #pragma unroll
   for (int u = 0; u < UN; ++u) {
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, PER * sizeof(T) <= 4 ? 1024 / THREADS
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) amax[u] = fmaxf(amax[u], red[u][w]);
     float after, inv;
-    page_scale(amax[u], before[u], after, inv);
+    page_scale(amax[u], lo > 0, before[u], after, inv);
     uint8_t* codes = p.codes[which] + page * p.page_stride + head * p.head_stride;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   if (mine) load(row0);
   if (!page_exists(p, part) || !has) return;
   float* scale = p.scale[which] + part.page * p.scale_page + head * p.scale_head;
-  const float before = part.lo > 0 ? read_scale(*scale) : 0.f;
+  float before = part.lo > 0 ? *scale : 0.f;
   float x[16], amax = 0.f;
   if (mine) {
     value(x);
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   float after, inv;
-  page_scale(amax, before, after, inv);
+  page_scale(amax, part.lo > 0, before, after, inv);
   uint8_t* codes = p.codes[which] + part.page * p.page_stride + head * p.head_stride;
   if (mine) {
     write8(codes + row0 * p.token_stride + sl.c0, x, inv);
