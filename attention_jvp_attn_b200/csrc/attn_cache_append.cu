@@ -18,9 +18,11 @@
 // reads depend on one another: the sequence, then its page beside the values and
 // the tables' rows, then the page's scale.
 // Bound by instructions and latency for prompts (32,800 tokens in pages of 16, 8
-// heads, d = 128, 210 MB: 52 us, 4.0 TB/s, 61 % of the copy rate; 63 us with the
+// heads, d = 128, 210 MB: 54 us, 3.9 TB/s, 59 % of the copy rate; 63 us with the
 // values read after the page, 129 us with one unit per block and 8 columns a
-// thread besides), by the three reads for single tokens (64 sequences: 2.9 us).
+// thread besides; fp32, 344 MB: 59 us), by the three reads for single tokens (64
+// sequences: 2.9 us, fp32 3.2). A chunk of 1,560 tokens, 12 heads, pages of 64: 5.9
+// us (fp32 8.4), some 624 blocks where 592 fit at once.
 #include "rope_slots.cuh"
 
 namespace ajvp_serve {
@@ -322,7 +324,12 @@ __global__ void __launch_bounds__(kFewWarps * 32)
 //   64 sequences, pages of 64:   1: 2.9 / 7.4   4: 3.0 / 7.8   8: 4.2 / 8.3   32: 9.2 / 10.4
 //   500 sequences, pages of 32:  1: 13 / 30     4: 14 / 33     8: 18 / 35     32: 51 / 58
 //   1 sequence, pages of 64:     1: 2.6 / 2.6   4: 2.7 / 2.7   8: 3.4 / 2.6   32: 7.4 / 2.7
-// Beyond it one long sequence would wait for its rounds.
+// Beyond it one long sequence would wait for its rounds. The mean decides, as the
+// host knows no lengths, so a chunk among single tokens may have to do just that, in
+// up to 32 rounds a page: sequences of one token and one of n, 8 heads, d = 128, us:
+//   pages of 16:   63 + one of 190: 4.8 / 4.0     255 + one of 760: 8.1 / 10.6   1,023 + one of 3,000: 36 / 49
+//   pages of 64:   63 + one of 190: 9.5 / 7.8     255 + one of 760: 14 / 24      1,023 + one of 3,000: 35 / 121
+//   pages of 128:  63 + one of 190: 16 / 12       255 + one of 760: 24 / 40      1,023 + one of 3,000: 45 / 208
 constexpr int kFewTokens = 4;
 
 // 32 values a thread in flight (64 for the largest pages), whatever the page.

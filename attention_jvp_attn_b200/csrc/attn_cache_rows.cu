@@ -42,7 +42,7 @@
 // Measured (one B200, d = 128): 64 sequences of 500 to 8,192 tokens, 32 query and 8
 // key heads, 586 MB: 112 us, 5.2 TB/s, 80 % of the copy rate (query rows as the
 // instruction's rows, codes copied by the lanes: 241 us); 3 sequences of 40,000 to
-// 131,072 tokens, 16 rows, 592 MB: 134 us, 4.4 TB/s.
+// 131,072 tokens, 16 rows, 592 MB: 133 us, 4.4 TB/s.
 #include <cuda.h>
 
 #include "serve_attn.cuh"
@@ -748,17 +748,20 @@ cudaError_t cache_rows_launch(const RowsParams& p, int d, int dtype, int blocks,
   return d == 128 ? rows_launch<__half, 128>(p, blocks, st) : rows_launch<__half, 64>(p, blocks, st);
 }
 
-// Blocks that share out the steps: as many per SM as fit (8 rows: 168 registers
-// and 70 KB; 16 rows: 255 and 104 KB. At 16 rows three blocks per SM spill and
+// Blocks that share out the steps: as many per SM as fit (8 rows: 168 registers,
+// 12 bytes spilled at d = 128, and 70 KB; 16 rows: 255 and 104 KB. At 16 rows three blocks per SM spill and
 // took 231 us where two take 134).
 constexpr int blocks_per_sm(int64_t rows) { return rows <= 8 ? 3 : 2; }
 
 // How the work of a call with `rows` query rows per key head is shared out, for
 // sequences of up to `len` tokens: blocks (0: clusters, no workspace) and bytes
 // of workspace for each.
-//   - More than 16 rows go to the tcgen05 kernel: 8 sequences of 8,192 tokens, 8
-//     key heads, d = 128: 33 us at 4 rows and 45 us at 16 here, 88 us at 20 rows
-//     and 99 us at 128 there (two passes over 16 rows here would take 90 us).
+//   - More than 16 rows go to the tcgen05 kernel. 8 sequences of 8,192 tokens, 8
+//     key heads, us of the GPU in a graph, d = 128 (64), here: 4 rows 34 (25), 8: 35
+//     (25), 9: 44 (34), 16: 46 (34); there: 17 and 20 rows 89 (72), 32: 90 (72), 64:
+//     94 (73), 128: 99 (76), 129: 115 (89), 256: 124 (93). A second call here for
+//     the rows beyond 16 would bring 17 to 24 rows to 81 (59) and 25 to 32 to 91
+//     (68), and three or more calls are behind.
 //   - Up to 16 rows, clusters (one launch) up to 512 tokens, or 4,096 if they are
 //     all resident at once; shared out evenly (two launches) beyond. us, clusters
 //     / shared out, single tokens, d = 128, by sequences x key heads and tokens:

@@ -21,9 +21,12 @@
 // a second, small kernel joins them.
 //
 // Measured (one B200): 1,560 queries over 32,760 tokens, 12 heads, d = 128, 314
-// GFLOP: 412 us, 760 TFLOP/s. The bound is the chain scores -> softmax -> products
-// of a row tile, 4,100 to 4,600 cycles per key tile against 2,048 of tensor work;
-// the conversion is beside it (without it the time is the same).
+// GFLOP: 409 to 426 us, 740 to 770 TFLOP/s (418 at a median of 1,935 MHz), causal
+// or not; 1,536 queries, which fill their row tiles, 359 us. The bound is the chain
+// scores -> softmax -> products of a row tile, 4,100 to 4,600 cycles per key tile
+// against 2,048 of tensor work; the conversion is beside it (without it the time is
+// the same). With one row tile (17 to 128 rows) nothing runs beside that chain: see
+// Share in attn_cache_rows.cu.
 //
 // NaN values of tokens that some rows must not see are taken out of the
 // product and marked, as in attn_prompt.cu; a row that sees a marked token

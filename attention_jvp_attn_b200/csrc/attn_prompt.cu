@@ -22,9 +22,13 @@
 // Key tiles behind a row tile's last row are never visited. The first half of a
 // tile's probabilities is handed to the products before the second half is
 // formed. Measured (one B200, bf16): 32,760 tokens, 8 query and 2 key heads, d =
-// 128: 1.52 to 1.82 ms, 1,210 to 1,440 TFLOP/s by the power-capped clock; five
-// prompts of 61 to 8,192 tokens: 0.56 to 0.66 ms; 1,333 tokens, d = 64: 17.3 us. A
-// pair of key tiles takes 3,200 cycles, 2,048 of them tensor work.
+// 128: 1.77 ms, 1,240 TFLOP/s, in a long row of calls (median 1,582 MHz, power-capped;
+// the first ten after a pause, at up to 1,965 MHz, 1.54 ms); five prompts of 61 to
+// 8,192 tokens: 0.64 ms (1,687 MHz; 0.59); 1,333 tokens, d = 64: 17.3 us. A pair of
+// key tiles takes 3,200 cycles, 2,048 of them tensor work. d = 64: 32,760 tokens 1.39
+// ms, 790 TFLOP/s (1,957 MHz), bound by the exponentials. Many short prompts are
+// bound by the blocks' start and end, one block per SM: 40 of 16 to 200 tokens, 16
+// heads, 36 us at d = 64 and 47 at 128.
 //
 // A masked key's probability is 0, but 0 times an infinity or NaN among its
 // values is not. So non-finite values in the tiles on the diagonal (which hold
@@ -547,9 +551,13 @@ extern "C" int attn_jvp_prompt_attn(const attn_jvp_tokens* shape, const void* q,
   p.T = static_cast<int>(s.T), p.B = static_cast<int>(B), p.H = static_cast<int>(s.H);
   p.group = static_cast<int>(s.H / s.Hkv);
   // Blocks of one row tile where blocks of two would not fill the SMs (they read
-  // each key twice as often). us, one / two, d = 64, by length and heads:
-  //   300 x 4: 8.6 / 9.2    1,333 x 16: 17.3 / 21.7   4,000 x 8: 34.8 / 54.8   8,000 x 4: 53.6 / 99.8
-  //   2,600 x 16: 39.3 / 37.4   4,000 x 16: 68.2 / 58.2   8 of 500, 8 heads: 17.7 / 13.8
+  // each key twice as often). us, one / two, by length and heads:
+  //                       d = 64         d = 128                       d = 64         d = 128
+  //   300 x 4:            8.8 / 9.1      9.8 / 12.3   2,600 x 16:      39.1 / 37.5    50.0 / 41.5
+  //   2 of 300, 16 heads: 9.2 / 9.6     10.1 / 12.6   4,000 x 16:      69.0 / 58.7    90.4 / 66.9
+  //   1,333 x 16:        17.3 / 21.8    21.7 / 25.0   1,300 x 32:      30.3 / 26.6    38.8 / 32.5
+  //   4,000 x 8:         34.7 / 54.3    45.1 / 57.7   8 of 500, 8 heads: 17.7 / 14.0  21.5 / 16.4
+  //   8,000 x 4:         53.6 / 99.5    69.3 / 104
   const bool single = pieces * s.H <= sms;
   if (single) pieces = s.T / kTile + B;
   p.pieces = static_cast<int>(pieces);

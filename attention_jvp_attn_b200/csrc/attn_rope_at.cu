@@ -12,11 +12,13 @@
 // Bound by HBM: each value is read and written once; the tables' row of a token
 // comes from L1 or L2 for all heads but the first. The position, then the
 // table's row, are two reads one after the other, so many warps are wanted; and
-// a thread keeps its columns' cosines and sines over its heads. Measured (one
-// B200): 32,760 tokens of 24 heads, d = 128, bf16, 419 MB: 77 us, 5.44 TB/s, 83 %
-// of the copy rate; with 8 columns of one head a thread 104 us (126 instructions
-// per 8 values), with a block per token that walks on to the next 107 us. 64
-// tokens of 40 heads: 3.1 us.
+// a thread keeps its columns' cosines and sines over its heads. Three blocks per
+// SM, so 80 registers, spill 20 to 28 bytes a thread (fp32: 76 to 104). Measured (one
+// B200): 32,760 tokens of 24 heads, d = 128, bf16, 419 MB: 75 to 77 us, 5.44 TB/s, 83
+// % of the copy rate (half layout: 73); with 8 columns of one head a thread 104 us
+// (126 instructions per 8 values), with a block per token that walks on to the next
+// 107 us. fp32, 822 MB: 155 us, 5.3 TB/s (half layout, whose runs of 8 columns a warp
+// reads side by side: 128 us, 6.4 TB/s). 64 tokens of 40 heads: 3.0 us (fp32 4.6).
 #include "rope_slots.cuh"
 
 namespace ajvp_serve {

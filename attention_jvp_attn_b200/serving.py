@@ -21,6 +21,11 @@ All arithmetic of the operators runs in the CUDA library behind the C ABI
 (include/attn_jvp.h); a binding in C++ (csrc/serve_binding.cpp) checks tensors
 and passes pointers, strides and the current stream. Positions, lengths and page numbers live on the
 device; one that is out of range is not used, and sync_status() then returns 7.
+
+As the package's other functions, none of these is registered with autograd: results carry
+no graph, whatever the inputs require. The gradient of rope_at is rope_at(..., transpose=True).
+Sums, maxima and LSE of the attentions are in 32 bits, probabilities in 16 (prompt_attn:
+the inputs' type; cache_attn: fp16, the page's value scale included).
 """
 from __future__ import annotations
 
@@ -98,6 +103,11 @@ def rope_tables(rot: int, n_positions: int, base: float = 10000.0, scaling: Opti
                  original_positions kept, those with at most slow_turns divided
                  by factor, a linear ramp over their index between; both tables
                  times `magnitude`, by default 0.1 ln(factor) + 1.
+
+    "base" is the published NTK-aware change of base, "by_parts" the published YaRN
+    method. So that tables agree with those of other programs two of its conventions
+    are kept: the ramp's upper index is bounded by rot - 1 (indices end at rot/2 - 1),
+    and its width is at least 1e-3.
     """
     if rot < 16 or rot % 16:
         raise ValueError("rot must be a positive multiple of 16")
